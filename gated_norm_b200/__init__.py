@@ -5,6 +5,14 @@ is a thin binding over it.  Importing the package loads the library and fails lo
 has not been built (``python gated_norm_b200/build.py``): there is no CPU fallback.
 """
 from .autograd import GatedRMSNorm, GatedRMSNormFunction, gated_rmsnorm  # noqa: F401
+from .block import (  # noqa: F401
+    BlockRMSNorm,
+    BlockRMSNormFunction,
+    block_rmsnorm,
+    gnorm_block_bwd,
+    gnorm_block_bwd_workspace_bytes,
+    gnorm_block_fwd,
+)
 from .gnorm import (  # noqa: F401
     GnormError,
     gnorm_build_info,

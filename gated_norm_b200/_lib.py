@@ -89,6 +89,46 @@ class GnormBwdDesc(ctypes.Structure):
     ]
 
 
+class GnormBlockFwdDesc(ctypes.Structure):
+    """Mirror of ``gnorm_block_fwd_desc`` in include/gnorm.h."""
+
+    _fields_ = [
+        ("a", ctypes.c_void_p), ("lda", ctypes.c_int64),
+        ("r", ctypes.c_void_p), ("ldr", ctypes.c_int64),
+        ("g", ctypes.c_void_p), ("ldg", ctypes.c_int64),
+        ("w1", ctypes.c_void_p), ("w2", ctypes.c_void_p),
+        ("w_fp32", ctypes.c_int), ("res_fp32", ctypes.c_int),
+        ("alpha", ctypes.c_void_p), ("eps1", ctypes.c_float), ("eps2", ctypes.c_float),
+        ("h", ctypes.c_void_p), ("ldh", ctypes.c_int64),
+        ("z", ctypes.c_void_p), ("ldz", ctypes.c_int64),
+        ("rstd1", ctypes.c_void_p), ("rstd2", ctypes.c_void_p),
+        ("M", ctypes.c_int64), ("N", ctypes.c_int64),
+    ]
+
+
+class GnormBlockBwdDesc(ctypes.Structure):
+    """Mirror of ``gnorm_block_bwd_desc`` in include/gnorm.h."""
+
+    _fields_ = [
+        ("dh", ctypes.c_void_p), ("lddh", ctypes.c_int64),
+        ("dz", ctypes.c_void_p), ("lddz", ctypes.c_int64),
+        ("a", ctypes.c_void_p), ("lda", ctypes.c_int64),
+        ("r", ctypes.c_void_p), ("ldr", ctypes.c_int64),
+        ("g", ctypes.c_void_p), ("ldg", ctypes.c_int64),
+        ("w1", ctypes.c_void_p), ("w2", ctypes.c_void_p),
+        ("w_fp32", ctypes.c_int), ("res_fp32", ctypes.c_int),
+        ("alpha", ctypes.c_void_p),
+        ("rstd1", ctypes.c_void_p), ("rstd2", ctypes.c_void_p),
+        ("da", ctypes.c_void_p), ("ldda", ctypes.c_int64),
+        ("dr", ctypes.c_void_p), ("lddr", ctypes.c_int64),
+        ("dg", ctypes.c_void_p), ("lddg", ctypes.c_int64),
+        ("dw1", ctypes.c_void_p), ("dw2", ctypes.c_void_p), ("dw_fp32", ctypes.c_int),
+        ("dalpha", ctypes.c_void_p),
+        ("M", ctypes.c_int64), ("N", ctypes.c_int64),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
 _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
 _int = ctypes.c_int
@@ -116,6 +156,9 @@ SIGNATURES = {
     "gnorm_dw_reduce": (_int, [_vp, _i64, _i64, _vp, _int, _vp]),
     "gnorm_bwd_workspace_bytes": (_sz, [_i64, _i64, _int]),
     "gnorm_bwd_workspace_bytes_for": (_sz, [_i64, _i64, _int, _int]),
+    "gnorm_block_fwd": (_int, [ctypes.POINTER(GnormBlockFwdDesc), _vp]),
+    "gnorm_block_bwd": (_int, [ctypes.POINTER(GnormBlockBwdDesc), _vp]),
+    "gnorm_block_bwd_workspace_bytes": (_sz, [_i64, _i64]),
     "gnorm_status_string": (ctypes.c_char_p, [_int]),
     "gnorm_plan_query": (_int, [_int, _i64, _i64, _int, _int, _int, ctypes.POINTER(GnormPlan)]),
     "gnorm_device_error": (_int, [_int]),

@@ -13,6 +13,7 @@
 #include <mutex>
 
 #include "args.h"
+#include "checks.h"
 #include "device_common.cuh"
 #include "gnorm.h"
 #include "layout.h"
@@ -42,15 +43,10 @@ namespace {
 constexpr int64_t kMaxRows = int64_t(1) << 40;
 constexpr int kMaxDevices = 64;
 
-struct DeviceInfo {
-  bool ready = false;
-  int num_sms = 0;
-  int smem_optin = 0;
-  unsigned* err_word = nullptr;
-};
-
 std::mutex g_dev_mu;
 DeviceInfo g_dev[kMaxDevices];
+
+}  // namespace
 
 int device_info(DeviceInfo* out) {
   int dev = 0;
@@ -73,8 +69,6 @@ int device_info(DeviceInfo* out) {
   return GNORM_OK;
 }
 
-}  // namespace
-
 // The current device's error word (device address), for entry points in other files.
 int device_error_word(unsigned** out) {
   DeviceInfo d;
@@ -86,70 +80,11 @@ int device_error_word(unsigned** out) {
 
 namespace {
 
-// A memory region an argument covers: a plain byte span, or a BF16 [rows, cols] matrix
-// with row stride `ld` elements.
-struct Region {
-  const void* p;
-  size_t bytes;     // whole extent
-  bool is_mat;
-  int64_t rows, cols, ld;
-};
-
-Region span(const void* p, size_t bytes) { return Region{p, bytes, false, 0, 0, 0}; }
-Region mat(const void* p, int64_t rows, int64_t cols, int64_t ld) {
-  const size_t bytes = rows > 0 ? static_cast<size_t>((rows - 1) * ld + cols) * 2 : 0;
-  return Region{p, bytes, true, rows, cols, ld};
-}
-
-int64_t floor_div(int64_t a, int64_t b) { return a / b - ((a % b != 0) && ((a < 0) != (b < 0))); }
-
-// Exact for two matrices with the same stride and width (their elements interleave
-// row by row); whole-extent overlap otherwise.
-bool overlaps(const Region& a, const Region& b) {
-  if (a.p == nullptr || b.p == nullptr || a.bytes == 0 || b.bytes == 0) return false;
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), a1 = a0 + a.bytes;
-  const uintptr_t b0 = reinterpret_cast<uintptr_t>(b.p), b1 = b0 + b.bytes;
-  if (!(a0 < b1 && b0 < a1)) return false;
-  if (!(a.is_mat && b.is_mat && a.ld == b.ld && a.cols == b.cols)) return true;
-  const int64_t diff = static_cast<int64_t>(b0 - a0);  // two's complement difference
-  if (diff % 2 != 0) return true;
-  const int64_t d = diff / 2, L = a.ld, n = a.cols;
-  const int64_t q = floor_div(d, L), delta = d - q * L;  // b's row j starts in a's row q + j
-  auto rows_meet = [&](int64_t off) { return off < a.rows && off + b.rows > 0; };
-  if (delta < n && rows_meet(q)) return true;          // columns [delta, n) of the same row
-  if (delta + n > L && rows_meet(q + 1)) return true;  // b's row runs into a's next row
-  return false;
-}
-
-// Every output region against every input region and every other output region.
-bool any_alias(const Region* in, int n_in, const Region* out, int n_out) {
-  for (int i = 0; i < n_out; ++i) {
-    for (int j = 0; j < n_in; ++j)
-      if (overlaps(out[i], in[j])) return true;
-    for (int j = i + 1; j < n_out; ++j)
-      if (overlaps(out[i], out[j])) return true;
-  }
-  return false;
-}
-
-// Row stride in elements: 0 means packed (N); a stride must hold a row and keep rows
-// 16-byte aligned.
-int check_ld(int64_t* ld, int64_t N) {
-  if (*ld == 0) *ld = N;
-  if (*ld < N) return GNORM_ERR_SHAPE;
-  if (*ld % 8 != 0) return GNORM_ERR_ALIGN;
-  return GNORM_OK;
-}
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
 int check_shape(int64_t M, int64_t N) {
   if (M < 0 || M > kMaxRows) return GNORM_ERR_SHAPE;
   if (N < 8 || N > GNORM_N_MAX || (N % 8) != 0) return GNORM_ERR_SHAPE;
   return GNORM_OK;
 }
-
-bool use_pdl() { return get_tuning().disable_pdl == 0; }
 
 // cuTensorMapEncodeTiled, fetched from the driver through the runtime (no libcuda link).
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
@@ -187,8 +122,6 @@ bool rows_map(CUtensorMap* map, const void* base, int64_t M, int64_t N, int64_t 
             box, elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-
-cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
 
 // `prefetch`: the previous kernel on the stream is known to write none of this call's
 // inputs, so the kernel may start copying them before that kernel has finished.

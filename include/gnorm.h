@@ -285,6 +285,97 @@ GNORM_API size_t gnorm_bwd_workspace_bytes(int64_t M, int64_t N, int determinist
 /* The same for a device with `num_sms` SMs.  Pure host function; needs no GPU. */
 GNORM_API size_t gnorm_bwd_workspace_bytes_for(int64_t M, int64_t N, int deterministic, int num_sms);
 
+/*
+ * The norm after a block, its gate, the residual scale and the norm before the next block in
+ * one pass.  For a row a of the block's output, residual r, gate g and weights w1, w2:
+ *
+ *     b = a * rsqrt(mean(a^2) + eps1) * w1
+ *     h = r + alpha * g * sigmoid(g) * b           (BF16 or FP32, as r)
+ *     z = h * rsqrt(mean(h^2) + eps2) * w2         (BF16; from h before it is rounded)
+ *
+ * a, g, z are BF16 [M, N]; r and h are BF16, or FP32 if res_fp32; w1 and w2 are BF16, or both
+ * FP32 if w_fp32; alpha is one FP32 value in device memory (4-byte aligned), NULL = 1; g NULL
+ * = no gate (the factor g sigmoid(g) is left out).  rstd1 and rstd2 [M] FP32 are the two row
+ * factors, kept for the backward.  Row strides as for gnorm_fwd_ex (elements; 0 = N).  h must
+ * not overlap r.  The other rules are those at the top of this file.
+ */
+typedef struct gnorm_block_fwd_desc {
+  const void* a;
+  int64_t lda;
+  const void* r;
+  int64_t ldr;
+  const void* g;
+  int64_t ldg;
+  const void* w1;
+  const void* w2;
+  int w_fp32;
+  int res_fp32;
+  const float* alpha;
+  float eps1;
+  float eps2;
+  void* h;
+  int64_t ldh;
+  void* z;
+  int64_t ldz;
+  float* rstd1;
+  float* rstd2;
+  int64_t M;
+  int64_t N;
+} gnorm_block_fwd_desc;
+
+GNORM_API int gnorm_block_fwd(const gnorm_block_fwd_desc* desc, void* stream);
+
+/*
+ * Its backward.  From dh (the gradient of h through the residual; NULL = zero) and dz (of z):
+ * da and dg (BF16), dr (BF16 or FP32, as r; it is the whole gradient of h), dw1 and dw2 [N]
+ * (FP32 if dw_fp32, else BF16) and dalpha (one FP32 value; may be NULL).  dh has r's type.
+ * a, r, g, w1, w2, alpha as given to the forward, rstd1 and rstd2 as it wrote them; h is not
+ * needed (it is computed again from r).  dg is NULL exactly where g is.  The sums over rows
+ * are FP32 in a fixed order: bitwise the same from run to run on one device model.  M == 0
+ * writes zero to dw1, dw2 and dalpha.
+ *
+ * workspace: gnorm_block_bwd_workspace_bytes(M, N) bytes, GNORM_WORKSPACE_ALIGN-aligned; it
+ * needs no initialisation.  Calls that may overlap on the GPU must not share one.
+ */
+typedef struct gnorm_block_bwd_desc {
+  const void* dh;
+  int64_t lddh;
+  const void* dz;
+  int64_t lddz;
+  const void* a;
+  int64_t lda;
+  const void* r;
+  int64_t ldr;
+  const void* g;
+  int64_t ldg;
+  const void* w1;
+  const void* w2;
+  int w_fp32;
+  int res_fp32;
+  const float* alpha;
+  const float* rstd1;
+  const float* rstd2;
+  void* da;
+  int64_t ldda;
+  void* dr;
+  int64_t lddr;
+  void* dg;
+  int64_t lddg;
+  void* dw1;
+  void* dw2;
+  int dw_fp32;
+  float* dalpha;
+  int64_t M;
+  int64_t N;
+  void* workspace;
+  size_t workspace_bytes;
+} gnorm_block_bwd_desc;
+
+GNORM_API int gnorm_block_bwd(const gnorm_block_bwd_desc* desc, void* stream);
+
+/* Workspace bytes gnorm_block_bwd needs on the CURRENT device (0 on invalid arguments). */
+GNORM_API size_t gnorm_block_bwd_workspace_bytes(int64_t M, int64_t N);
+
 /* Human-readable name of a gnorm_status value (static storage). */
 GNORM_API const char* gnorm_status_string(int status);
 
