@@ -122,10 +122,12 @@ def measured_peaks():
         return FALLBACK_HBM_GBS, "fallback"
 
 
-# Host code of entry points bench.py does not call (the kernels, and the code that plans
-# and launches them for bench.py, live in the other files): a change there leaves recorded
-# ncu counters valid.
-_DIGEST_EXCLUDED = ("host_step.cu", "noalloc.cu")
+# Code of entry points bench.py does not call (the kernels it runs, and the code that plans
+# and launches them, live in the other files): a change there leaves recorded ncu counters
+# valid.
+_DIGEST_EXCLUDED = ("host_step.cu", "noalloc.cu", "block.cu", "block_kernel.cuh", "delta.cu",
+                    "delta_common.cuh", "delta_grad.cuh", "delta_prep.cuh", "delta_scan.cuh",
+                    "delta_step.cuh")
 
 
 def _code_only(text):

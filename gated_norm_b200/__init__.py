@@ -13,6 +13,15 @@ from .block import (  # noqa: F401
     gnorm_block_bwd_workspace_bytes,
     gnorm_block_fwd,
 )
+from .delta import (  # noqa: F401
+    GatedDeltaNorm,
+    GatedDeltaRuleFunction,
+    gated_delta_rule,
+    gnorm_delta_bwd,
+    gnorm_delta_fwd,
+    gnorm_delta_step,
+    gnorm_delta_workspace_bytes,
+)
 from .gnorm import (  # noqa: F401
     GnormError,
     gnorm_build_info,

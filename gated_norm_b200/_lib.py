@@ -129,6 +129,74 @@ class GnormBlockBwdDesc(ctypes.Structure):
     ]
 
 
+class GnormDeltaIn(ctypes.Structure):
+    """Mirror of ``gnorm_delta_in`` in include/gnorm.h."""
+
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("ldq", ctypes.c_int64),
+        ("k", ctypes.c_void_p), ("ldk", ctypes.c_int64),
+        ("v", ctypes.c_void_p), ("ldv", ctypes.c_int64),
+        ("g", ctypes.c_void_p), ("ldg", ctypes.c_int64),
+        ("beta", ctypes.c_void_p), ("ldbeta", ctypes.c_int64),
+        ("beta_fp32", ctypes.c_int),
+        ("cu_seqlens", ctypes.c_void_p),
+        ("B", ctypes.c_int64), ("T", ctypes.c_int64),
+        ("Hk", ctypes.c_int64), ("Hv", ctypes.c_int64),
+        ("K", ctypes.c_int64), ("V", ctypes.c_int64),
+        ("scale", ctypes.c_float),
+        ("initial_state", ctypes.c_void_p),
+    ]
+
+
+class GnormDeltaFwdDesc(ctypes.Structure):
+    """Mirror of ``gnorm_delta_fwd_desc`` in include/gnorm.h."""
+
+    _fields_ = [
+        ("in", GnormDeltaIn),
+        ("o", ctypes.c_void_p), ("ldo", ctypes.c_int64),
+        ("final_state", ctypes.c_void_p),
+        ("zero_tail", ctypes.c_int),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class GnormDeltaBwdDesc(ctypes.Structure):
+    """Mirror of ``gnorm_delta_bwd_desc`` in include/gnorm.h."""
+
+    _fields_ = [
+        ("in", GnormDeltaIn),
+        ("d_o", ctypes.c_void_p), ("lddo", ctypes.c_int64),
+        ("dfinal_state", ctypes.c_void_p),
+        ("dq", ctypes.c_void_p), ("lddq", ctypes.c_int64),
+        ("dk", ctypes.c_void_p), ("lddk", ctypes.c_int64),
+        ("dv", ctypes.c_void_p), ("lddv", ctypes.c_int64),
+        ("dg", ctypes.c_void_p), ("lddg", ctypes.c_int64),
+        ("dbeta", ctypes.c_void_p), ("lddbeta", ctypes.c_int64),
+        ("dinitial_state", ctypes.c_void_p),
+        ("zero_tail", ctypes.c_int),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class GnormDeltaStepDesc(ctypes.Structure):
+    """Mirror of ``gnorm_delta_step_desc`` in include/gnorm.h."""
+
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("ldq", ctypes.c_int64),
+        ("k", ctypes.c_void_p), ("ldk", ctypes.c_int64),
+        ("v", ctypes.c_void_p), ("ldv", ctypes.c_int64),
+        ("g", ctypes.c_void_p), ("ldg", ctypes.c_int64),
+        ("beta", ctypes.c_void_p), ("ldbeta", ctypes.c_int64),
+        ("beta_fp32", ctypes.c_int),
+        ("B", ctypes.c_int64), ("Hk", ctypes.c_int64), ("Hv", ctypes.c_int64),
+        ("K", ctypes.c_int64), ("V", ctypes.c_int64),
+        ("scale", ctypes.c_float),
+        ("state", ctypes.c_void_p), ("ldstate", ctypes.c_int64), ("pool", ctypes.c_int64),
+        ("slots", ctypes.c_void_p),
+        ("o", ctypes.c_void_p), ("ldo", ctypes.c_int64),
+    ]
+
+
 _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
 _int = ctypes.c_int
@@ -159,6 +227,10 @@ SIGNATURES = {
     "gnorm_block_fwd": (_int, [ctypes.POINTER(GnormBlockFwdDesc), _vp]),
     "gnorm_block_bwd": (_int, [ctypes.POINTER(GnormBlockBwdDesc), _vp]),
     "gnorm_block_bwd_workspace_bytes": (_sz, [_i64, _i64]),
+    "gnorm_delta_fwd": (_int, [ctypes.POINTER(GnormDeltaFwdDesc), _vp]),
+    "gnorm_delta_bwd": (_int, [ctypes.POINTER(GnormDeltaBwdDesc), _vp]),
+    "gnorm_delta_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64, _i64, _int]),
+    "gnorm_delta_step": (_int, [ctypes.POINTER(GnormDeltaStepDesc), _vp]),
     "gnorm_status_string": (ctypes.c_char_p, [_int]),
     "gnorm_plan_query": (_int, [_int, _i64, _i64, _int, _int, _int, ctypes.POINTER(GnormPlan)]),
     "gnorm_device_error": (_int, [_int]),

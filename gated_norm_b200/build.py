@@ -29,7 +29,7 @@ LIB = os.path.join(PKG, "libgnorm.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 SOURCES = ["api.cu", "fwd.cu", "bwd.cu", "plan.cpp", "noalloc.cu", "host_step.cu",
-           "block.cu"]
+           "block.cu", "delta.cu"]
 
 
 def nvcc() -> str:

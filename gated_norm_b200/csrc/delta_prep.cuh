@@ -1,0 +1,183 @@
+// delta_prep.cuh -- what a chunk of the gated delta rule needs apart from the state, for all
+// chunks at once: N = (I + Kb diag(beta))^-1 Kb, P and the decay factors (delta_common.cuh).
+//
+// One CTA per (chunk, key head): K K^T and Q K^T once (BF16 operands, exact, FP32 sums), then
+// for each value head of the group the decays, and N by forward substitution: column j of N
+// solves n_i = Kb_ij - sum_{l<i} Kb_il beta_l n_l.  Two neighbouring threads share a column,
+// each keeps half of its values in registers and reads the coefficients of row i from shared
+// memory (the same address for the whole warp), so no step waits for another warp.
+#pragma once
+
+#include "delta_common.cuh"
+
+namespace gnorm {
+
+constexpr int kPrepThreads = 128;
+constexpr int kKbLd = 68;  // floats of a row of Kb in shared memory
+
+template <int KD>
+GNORM_HD constexpr int prep_smem() {
+  // q and k tiles, reused for the tiles that go out; Kb; G; scalars
+  return (KD / 64 * 2 * kTileBytes > 4 * kTileBytes ? KD / 64 * 2 * kTileBytes : 4 * kTileBytes) +
+         64 * kKbLd * 4 + 64 * 8 + 1024;
+}
+
+template <int KD>
+__global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(const __grid_constant__ DeltaArgs a) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  constexpr int kTiles = KD / 64;
+  constexpr int kTileArea = kTiles * 2 * kTileBytes > 4 * kTileBytes ? kTiles * 2 * kTileBytes : 4 * kTileBytes;
+  float* kb = reinterpret_cast<float*>(smem + kTileArea);
+  double* Gs = reinterpret_cast<double*>(kb + 64 * kKbLd);
+  float* scal = reinterpret_cast<float*>(Gs + 64);  // beta, gamma, lambda [64], e^{G_C}
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const long long slot = blockIdx.x;
+  const int hk = blockIdx.y;
+  grid_dependency_wait();
+  allow_dependent_launch();
+  const int b = seq_of_slot(a.seq, slot, lane);
+  const long long chunk = slot - seq_base(a.seq, b);
+  const long long t0 = seq_start(a.seq, b) + chunk * kChunk;
+  const long long left = seq_end(a.seq, b) - t0;
+  if (chunk < 0 || left <= 0) return;
+  const int live = static_cast<int>(left < kChunk ? left : kChunk);
+  if (b == a.seq.B) {  // tokens behind the last sequence
+    if (hk != 0) return;
+    for (int z = 0; z < a.n_zero; ++z)
+      for (int r = warp; r < live; r += kPrepThreads / 32)
+        for (int i = lane * 2; i < a.zero_row[z]; i += 64)
+          *reinterpret_cast<uint16_t*>(a.zero_p[z] + (t0 + r) * a.zero_ld[z] + i) = 0;
+    return;
+  }
+  const uint32_t sq = smem_u32(smem), sk = sq + kTiles * kTileBytes;
+  load_rows<kPrepThreads>(sq, a.q + t0 * a.ldq + static_cast<long long>(hk) * KD, a.ldq, KD, live);
+  load_rows<kPrepThreads>(sk, a.k + t0 * a.ldk + static_cast<long long>(hk) * KD, a.ldk, KD, live);
+  cp_commit();
+  cp_wait<0>();
+  __syncthreads();
+
+  // rows 16 warp .. +15 of K K^T and Q K^T, columns up to the diagonal block
+  const int i0 = warp * 16;
+  float kk[8][4], qk[8][4];
+#pragma unroll
+  for (int n = 0; n < 8; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) kk[n][e] = qk[n][e] = 0.f;
+#pragma unroll
+  for (int kb16 = 0; kb16 < KD / 16; ++kb16) {
+    const uint32_t toff = (kb16 >> 2) * kTileBytes;
+    const int c0 = (kb16 & 3) * 16;
+    uint32_t ak[4], aq[4];
+    ldsm4(ak, addr_a(sk + toff, i0, c0, lane));
+    ldsm4(aq, addr_a(sq + toff, i0, c0, lane));
+#pragma unroll
+    for (int nb = 0; nb < 4; ++nb) {
+      if (nb <= warp) {
+        uint32_t bk[4];
+        ldsm4(bk, addr_b(sk + toff, nb * 16, c0, lane));
+        mma16816(kk[2 * nb], ak, bk[0], bk[1]);
+        mma16816(kk[2 * nb + 1], ak, bk[2], bk[3]);
+        mma16816(qk[2 * nb], aq, bk[0], bk[1]);
+        mma16816(qk[2 * nb + 1], aq, bk[2], bk[3]);
+      }
+    }
+  }
+  __syncthreads();  // the q and k tiles are free
+
+  const int group = a.Hv / a.Hk;
+  uint8_t* tiles = smem;  // N hi, N lo, P hi, P lo
+  for (int r = 0; r < group; ++r) {
+    const int h = hk * group + r;
+    if (warp == 0) {
+      // running sum of g in FP64: differences of far terms stay exact to FP32
+      const int ta = 2 * lane, tb = ta + 1;
+      const float ga = ta < live ? clamp_decay(a.g[(t0 + ta) * a.ldg + h]) : 0.f;
+      const float gb = tb < live ? clamp_decay(a.g[(t0 + tb) * a.ldg + h]) : 0.f;
+      double s = static_cast<double>(ga) + static_cast<double>(gb);
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const double o = __shfl_up_sync(0xffffffffu, s, off);
+        if (lane >= off) s += o;
+      }
+      const double total = __shfl_sync(0xffffffffu, s, 31);
+      const double Ga = s - static_cast<double>(gb);
+      Gs[ta] = Ga;
+      Gs[tb] = s;
+      scal[ta] = ta < live ? load_beta(a, t0 + ta, h) : 0.f;
+      scal[tb] = tb < live ? load_beta(a, t0 + tb, h) : 0.f;
+      scal[64 + ta] = expf(static_cast<float>(Ga));
+      scal[64 + tb] = expf(static_cast<float>(s));
+      scal[128 + ta] = expf(static_cast<float>(total - Ga));
+      scal[128 + tb] = expf(static_cast<float>(total - s));
+      if (lane == 0) scal[192] = expf(static_cast<float>(total));
+    }
+    __syncthreads();
+    // Kb (FP32, zero on and above the diagonal) and the P tiles
+    const int ra = i0 + (lane >> 2), rb = ra + 8;
+    const double Ga = Gs[ra], Gb = Gs[rb];
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+      const int c = n * 8 + 2 * (lane & 3);
+      const double G0 = Gs[c], G1 = Gs[c + 1];
+      float d[4] = {0.f, 0.f, 0.f, 0.f};
+      if (c <= ra) d[0] = expf(static_cast<float>(Ga - G0));
+      if (c + 1 <= ra) d[1] = expf(static_cast<float>(Ga - G1));
+      if (c <= rb) d[2] = expf(static_cast<float>(Gb - G0));
+      if (c + 1 <= rb) d[3] = expf(static_cast<float>(Gb - G1));
+      float p[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) p[e] = d[e] != 0.f ? qk[n][e] * d[e] : 0.f;
+      *reinterpret_cast<float2*>(kb + ra * kKbLd + c) =
+          make_float2(c < ra ? kk[n][0] * d[0] : 0.f, c + 1 < ra ? kk[n][1] * d[1] : 0.f);
+      *reinterpret_cast<float2*>(kb + rb * kKbLd + c) =
+          make_float2(c < rb ? kk[n][2] * d[2] : 0.f, c + 1 < rb ? kk[n][3] * d[3] : 0.f);
+      uint32_t hi, lo;
+      const uint32_t oa = tile_off(ra, n) + (c & 7) * 2, ob = tile_off(rb, n) + (c & 7) * 2;
+      split2(p[0], p[1], hi, lo);
+      *reinterpret_cast<uint32_t*>(tiles + 2 * kTileBytes + oa) = hi;
+      *reinterpret_cast<uint32_t*>(tiles + 3 * kTileBytes + oa) = lo;
+      split2(p[2], p[3], hi, lo);
+      *reinterpret_cast<uint32_t*>(tiles + 2 * kTileBytes + ob) = hi;
+      *reinterpret_cast<uint32_t*>(tiles + 3 * kTileBytes + ob) = lo;
+    }
+    __syncthreads();
+    // forward substitution, column tid / 2; this thread keeps beta_l n_l of the blocks of
+    // four rows l whose number has its parity
+    {
+      const int j = tid >> 1, par = tid & 1;
+      float x[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) x[i] = 0.f;
+#pragma unroll
+      for (int i = 0; i < 64; ++i) {
+        const float* row = kb + i * kKbLd;
+        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+        for (int m = 0; m < (i + 7) / 8; ++m) {
+          const float4 cf = *reinterpret_cast<const float4*>(row + (2 * m + par) * 4);
+          s0 = fmaf(cf.x, x[4 * m], s0);
+          s1 = fmaf(cf.y, x[4 * m + 1], s1);
+          s0 = fmaf(cf.z, x[4 * m + 2], s0);
+          s1 = fmaf(cf.w, x[4 * m + 3], s1);
+        }
+        s0 += s1;
+        s0 += __shfl_xor_sync(0xffffffffu, s0, 1);
+        const float n = row[j] - s0;
+        if (((i >> 2) & 1) == par) x[(i >> 3) * 4 + (i & 3)] = scal[i] * n;
+        const __nv_bfloat16 hi = __float2bfloat16_rn(n);
+        const __nv_bfloat16 out = par == 0 ? hi : __float2bfloat16_rn(n - __bfloat162float(hi));
+        *reinterpret_cast<__nv_bfloat16*>(tiles + par * kTileBytes + tile_off(i, j >> 3) +
+                                          (j & 7) * 2) = out;
+      }
+    }
+    __syncthreads();
+    uint8_t* dst = a.prep + (slot * a.Hv + h) * kPrepBytes;
+    for (int i = tid * 16; i < kPrepTiles; i += kPrepThreads * 16)
+      *reinterpret_cast<uint4*>(dst + i) = *reinterpret_cast<const uint4*>(tiles + i);
+    for (int i = tid; i < 193; i += kPrepThreads)
+      reinterpret_cast<float*>(dst + kPrepTiles)[i] = scal[i];
+    __syncthreads();
+  }
+}
+
+}  // namespace gnorm

@@ -376,6 +376,139 @@ GNORM_API int gnorm_block_bwd(const gnorm_block_bwd_desc* desc, void* stream);
 /* Workspace bytes gnorm_block_bwd needs on the CURRENT device (0 on invalid arguments). */
 GNORM_API size_t gnorm_block_bwd_workspace_bytes(int64_t M, int64_t N);
 
+/*
+ * The gated delta rule, the recurrence whose output a linear-attention layer hands to the
+ * gated norm.  Per sequence and value head, with a state S of K x V values:
+ *
+ *     S_t = exp(g_t) S_{t-1} + k_t u_t^T,  u_t = beta_t (v_t - exp(g_t) S_{t-1}^T k_t)
+ *     o_t = scale * S_t^T q_t
+ *
+ * q, k: BF16 [T, Hk, K]; v, o: BF16 [T, Hv, V]; g: FP32 [T, Hv] (the log of the decay, <= 0;
+ * values below -200, -inf among them, act as a full reset); beta: [T, Hv] BF16, or FP32 if
+ * beta_fp32.  K and V are 64 or 128, Hv a multiple of Hk (value head h uses key head
+ * h / (Hv / Hk)).  ld* = elements from one token to the next (0 = packed); heads are packed
+ * within a token; ldq, ldk, ldv, ldo and their gradients' are multiples of 8.  T tokens hold
+ * B sequences: cu_seqlens (int32 [B + 1] in device memory, not decreasing, cu[0] = 0, cu[B] <=
+ * T) or, if NULL, B of T / B tokens each.  A sequence may be empty.  Tokens behind the last
+ * sequence are not read; their rows of the outputs are left as they are, or set to zero if
+ * zero_tail.  States are FP32 [B, Hv, K, V].  T < 2^31; B, Hv <= 65535.
+ *
+ * States, the running sums of g and everything between the BF16 inputs and the outputs are
+ * held to FP32: matrix operands that are not exact in BF16 are split in two BF16 values.
+ * Results are bitwise the same from run to run.
+ */
+typedef struct gnorm_delta_in {
+  const void* q;
+  int64_t ldq;
+  const void* k;
+  int64_t ldk;
+  const void* v;
+  int64_t ldv;
+  const float* g;
+  int64_t ldg;
+  const void* beta;
+  int64_t ldbeta;
+  int beta_fp32;
+  const int* cu_seqlens;
+  int64_t B;
+  int64_t T;
+  int64_t Hk;
+  int64_t Hv;
+  int64_t K;
+  int64_t V;
+  float scale;
+  const float* initial_state; /* NULL = zero */
+} gnorm_delta_in;
+
+/*
+ * Forward: writes o and, unless NULL, final_state.  workspace:
+ * gnorm_delta_workspace_bytes(T, B, Hv, K, V, 0) bytes, GNORM_WORKSPACE_ALIGN-aligned, no
+ * initialisation needed; calls that may overlap on the GPU must not share one.
+ */
+typedef struct gnorm_delta_fwd_desc {
+  gnorm_delta_in in;
+  void* o;
+  int64_t ldo;
+  float* final_state;
+  int zero_tail;
+  void* workspace;
+  size_t workspace_bytes;
+} gnorm_delta_fwd_desc;
+
+GNORM_API int gnorm_delta_fwd(const gnorm_delta_fwd_desc* desc, void* stream);
+
+/*
+ * Backward: from d_o (the gradient of o) and dfinal_state (NULL = zero), with the forward's
+ * inputs, writes dq, dk, dv (BF16; dq and dk summed over the value heads of a key head), dg
+ * (FP32), dbeta (beta's type) and, unless NULL, dinitial_state.  The forward keeps nothing
+ * for it: chunk states are computed again.  workspace:
+ * gnorm_delta_workspace_bytes(T, B, Hv, K, V, 1) bytes (about 215 KB per 64 tokens and value
+ * head at K = V = 128).
+ */
+typedef struct gnorm_delta_bwd_desc {
+  gnorm_delta_in in;
+  const void* d_o;
+  int64_t lddo;
+  const float* dfinal_state;
+  void* dq;
+  int64_t lddq;
+  void* dk;
+  int64_t lddk;
+  void* dv;
+  int64_t lddv;
+  float* dg;
+  int64_t lddg;
+  void* dbeta;
+  int64_t lddbeta;
+  float* dinitial_state;
+  int zero_tail;
+  void* workspace;
+  size_t workspace_bytes;
+} gnorm_delta_bwd_desc;
+
+GNORM_API int gnorm_delta_bwd(const gnorm_delta_bwd_desc* desc, void* stream);
+
+/* Workspace bytes of the two calls above (0 on invalid arguments).  Needs no GPU. */
+GNORM_API size_t gnorm_delta_workspace_bytes(int64_t T, int64_t B, int64_t Hv, int64_t K,
+                                             int64_t V, int backward);
+
+/*
+ * One token of each of B sequences, the states updated in place: state is FP32
+ * [pool, Hv, K, V] with ldstate values from one slot to the next (0 = packed; a multiple of
+ * 4), row b's state is slot slots[b] (int32 [B] in device memory; NULL: slot b).  A row whose
+ * slot is negative or not below pool is padding: its o is set to zero, no state is touched.
+ * Rows that name the same slot are consecutive tokens of that sequence, in row order.  ldv
+ * and ldo are multiples of 4, v and o 8-byte aligned, q and k 2-byte aligned; the rest as
+ * above (T = B, one token a row).
+ */
+typedef struct gnorm_delta_step_desc {
+  const void* q;
+  int64_t ldq;
+  const void* k;
+  int64_t ldk;
+  const void* v;
+  int64_t ldv;
+  const float* g;
+  int64_t ldg;
+  const void* beta;
+  int64_t ldbeta;
+  int beta_fp32;
+  int64_t B;
+  int64_t Hk;
+  int64_t Hv;
+  int64_t K;
+  int64_t V;
+  float scale;
+  float* state;
+  int64_t ldstate;
+  int64_t pool;
+  const int* slots;
+  void* o;
+  int64_t ldo;
+} gnorm_delta_step_desc;
+
+GNORM_API int gnorm_delta_step(const gnorm_delta_step_desc* desc, void* stream);
+
 /* Human-readable name of a gnorm_status value (static storage). */
 GNORM_API const char* gnorm_status_string(int status);
 
