@@ -38,20 +38,25 @@ cudaError_t launch_prep(const DeltaArgs& a, cudaStream_t s) {
   return launch_grid(delta_prep_kernel<KD>, grid, kPrepThreads, prep_smem<KD>(), s, a);
 }
 
-template <int KD, bool kOut, bool kSave>
+// Strips of 16 columns a CTA.  One while they all fit on the SMs side by side, so that every
+// strip has an SM's four schedulers to itself; otherwise two, which share the right operands.
+int scan_groups(const DeltaArgs& a, int num_sms) {
+  return static_cast<long long>(a.V / 16) * a.Hv * a.seq.B <= num_sms ? 1 : 2;
+}
+
+template <int KD, int G, bool kOut, bool kSave>
 cudaError_t launch_scan_fwd(const DeltaArgs& a, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>(a.V / 64), static_cast<unsigned>(a.Hv),
+  const dim3 grid(static_cast<unsigned>(a.V / (16 * G)), static_cast<unsigned>(a.Hv),
                   static_cast<unsigned>(a.seq.B));
-  return launch_grid(delta_scan_fwd_kernel<KD, kOut, kSave>, grid, kScanThreads,
-                     2 * ScanStage<KD, false>::kBytes, s, a);
+  return launch_grid(delta_scan_fwd_kernel<KD, G, kOut, kSave>, grid, G * kStripThreads,
+                     scan_smem<KD, G, false>(), s, a);
 }
 
 template <int KD>
 cudaError_t launch_scan_bwd(const DeltaArgs& a, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>(a.V / 64), static_cast<unsigned>(a.Hv),
+  const dim3 grid(static_cast<unsigned>(a.V / 16), static_cast<unsigned>(a.Hv),
                   static_cast<unsigned>(a.seq.B));
-  return launch_grid(delta_scan_bwd_kernel<KD>, grid, kScanThreads,
-                     2 * ScanStage<KD, true>::kBytes, s, a);
+  return launch_grid(delta_scan_bwd_kernel<KD>, grid, kStripThreads, scan_smem<KD, 1, true>(), s, a);
 }
 
 template <int KD, int VD>
@@ -61,15 +66,19 @@ cudaError_t launch_grad(const DeltaArgs& a, cudaStream_t s) {
 }
 
 template <int KD>
-cudaError_t run_fwd(const DeltaArgs& a, cudaStream_t s) {
+cudaError_t run_fwd(const DeltaArgs& a, int num_sms, cudaStream_t s) {
   const cudaError_t e = launch_prep<KD>(a, s);
-  return e != cudaSuccess ? e : launch_scan_fwd<KD, true, false>(a, s);
+  if (e != cudaSuccess) return e;
+  return scan_groups(a, num_sms) == 1 ? launch_scan_fwd<KD, 1, true, false>(a, s)
+                                      : launch_scan_fwd<KD, 2, true, false>(a, s);
 }
 
 template <int KD>
-cudaError_t run_bwd(const DeltaArgs& a, cudaStream_t s) {
+cudaError_t run_bwd(const DeltaArgs& a, int num_sms, cudaStream_t s) {
   cudaError_t e = launch_prep<KD>(a, s);
-  if (e == cudaSuccess) e = launch_scan_fwd<KD, false, true>(a, s);
+  if (e != cudaSuccess) return e;
+  e = scan_groups(a, num_sms) == 1 ? launch_scan_fwd<KD, 1, false, true>(a, s)
+                                   : launch_scan_fwd<KD, 2, false, true>(a, s);
   if (e == cudaSuccess) e = launch_scan_bwd<KD>(a, s);
   if (e == cudaSuccess)
     e = a.V == 64 ? launch_grad<KD, 64>(a, s) : launch_grad<KD, 128>(a, s);
@@ -95,7 +104,7 @@ DeltaLayout delta_layout(int64_t T, int64_t B, int64_t Hv, int64_t K, int64_t V,
   if (backward) {
     l.s = take(static_cast<size_t>(K * V) * 4);
     l.d = take(static_cast<size_t>(K * V) * 4);
-    l.w = take(static_cast<size_t>(2 * V / 64) * kTileBytes);
+    l.w = take(static_cast<size_t>(3 * V / 64) * kTileBytes);
     l.x = take(static_cast<size_t>(V / 64) * kTileBytes);
     l.dots = take(static_cast<size_t>(V / 16) * 128 * 4);
   }
@@ -235,8 +244,11 @@ int gnorm_delta_fwd(const gnorm_delta_fwd_desc* desc, void* stream) {
   a.state_out = f.final_state;
   a.prep = static_cast<uint8_t*>(f.workspace) + l.prep;
   if (f.zero_tail && f.o) add_zero(&a, f.o, f.ldo, d.Hv * d.V, 2);
+  DeviceInfo info;
+  if ((st = device_info(&info)) != GNORM_OK) return st;
   const cudaStream_t s = as_stream(stream);
-  const cudaError_t e = d.K == 64 ? run_fwd<64>(a, s) : run_fwd<128>(a, s);
+  const cudaError_t e =
+      d.K == 64 ? run_fwd<64>(a, info.num_sms, s) : run_fwd<128>(a, info.num_sms, s);
   return e == cudaSuccess ? GNORM_OK : GNORM_ERR_CUDA;
 }
 
@@ -302,8 +314,11 @@ int gnorm_delta_bwd(const gnorm_delta_bwd_desc* desc, void* stream) {
     add_zero(&a, f.dg, f.lddg, d.Hv, 4);
     add_zero(&a, f.dbeta, f.lddbeta, d.Hv, d.beta_fp32 ? 4 : 2);
   }
+  DeviceInfo info;
+  if ((st = device_info(&info)) != GNORM_OK) return st;
   const cudaStream_t s = as_stream(stream);
-  const cudaError_t e = d.K == 64 ? run_bwd<64>(a, s) : run_bwd<128>(a, s);
+  const cudaError_t e =
+      d.K == 64 ? run_bwd<64>(a, info.num_sms, s) : run_bwd<128>(a, info.num_sms, s);
   return e == cudaSuccess ? GNORM_OK : GNORM_ERR_CUDA;
 }
 

@@ -17,12 +17,13 @@
 // (delta_prep_kernel); only the products with S run chunk after chunk (delta_scan kernels).
 //
 // Precision.  q, k, v and do are BF16, so they enter the tensor cores exactly.  States, N, P,
-// X, W and their gradients are FP32 values: as a matrix operand each is split into two BF16
-// values, hi = bf16(x) and lo = bf16(x - hi), and a product takes two instructions against an
-// exact operand and three against a split one (lo x lo, below 2^-16 of the product, is left
-// out).  That keeps 16 to 17 bits of every operand: an emulation of the whole chunked path in
-// this arithmetic is 3e-6 to 5e-6 (relative 2-norm) from FP64 in the states and FP32 gradients,
-// with single BF16 operands it is 2e-3, too far for FP32 outputs.
+// X, W and their gradients are FP32 values: as a matrix operand each is cut into BF16 parts,
+// p0 = bf16(x), p1 = bf16(x - p0), p2 = bf16(x - p0 - p1), and a product against an exact
+// operand takes an instruction per part, one of two cut operands the six products whose
+// weight is 2^-24 or more.  Three parts hold all 24 bits of an FP32 value, and with FP32 sums
+// the chunked form is as exact as FP32 arithmetic.  Two parts (16 to 17 bits) are not enough
+// for a state: where the terms of a sum take each other back (one key repeated), it was 4e-4
+// off.  Two parts remain where a product only reaches a BF16 output (o, dq, dk).
 #pragma once
 
 #include "device_common.cuh"
@@ -96,6 +97,15 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
   lo = pack_bf16x2(x - bf_lo(hi), y - bf_hi(hi));
 }
 
+// Two FP32 values as BF16 pairs: three parts, 24 bits.
+__device__ __forceinline__ void split3(float x, float y, uint32_t p[3]) {
+  p[0] = pack_bf16x2(x, y);
+  x -= bf_lo(p[0]);
+  y -= bf_hi(p[0]);
+  p[1] = pack_bf16x2(x, y);
+  p[2] = pack_bf16x2(x - bf_lo(p[1]), y - bf_hi(p[1]));
+}
+
 // A fragments (hi, lo) of a 16 x 16 block from two accumulator tiles 16 x 8 side by side.
 __device__ __forceinline__ void split_frag(const float t0[4], const float t1[4], uint32_t hi[4],
                                            uint32_t lo[4]) {
@@ -158,10 +168,18 @@ __device__ __forceinline__ int seq_of_slot(const DeltaSeqs& s, long long slot, i
 }
 inline long long delta_slots(long long T, long long B) { return T / kChunk + B + 1; }
 
-// Per (slot, value head): N and P as hi and lo tiles, beta, gamma, lambda [64] and e^{G_C}.
-constexpr long long kPrepTiles = 4LL * kTileBytes;
+// Per (slot, value head): N and P in three parts each, then beta, gamma, lambda [64] and
+// e^{G_C}.  Both are lower triangular; a part holds the 8 x 8 matrices (128 contiguous bytes,
+// an ldmatrix row group) of the 16 x 16 blocks on and below the diagonal: for each 8-row tile t
+// the column tiles 0 .. 2 (t / 2) + 1.
+GNORM_HD constexpr int tri_row(int t) { return 2 * (t / 2) * (t / 2 + 1) + (t & 1) * 2 * (t / 2 + 1); }
+constexpr int kTriBytes = 40 * 128;  // tri_row(8) matrices
+__device__ __forceinline__ uint32_t tri_off(int i, int j) {  // element (i, j)
+  return static_cast<uint32_t>((tri_row(i >> 3) + (j >> 3)) * 128 + (i & 7) * 16 + (j & 7) * 2);
+}
+constexpr long long kPrepTri = 6LL * kTriBytes;
 constexpr long long kPrepScal = 1024;
-constexpr long long kPrepBytes = kPrepTiles + kPrepScal;
+constexpr long long kPrepBytes = kPrepTri + kPrepScal;
 
 struct DeltaArgs {
   DeltaSeqs seq;
@@ -182,7 +200,7 @@ struct DeltaArgs {
   long long lddo = 0;
   uint8_t* s_ws = nullptr;  // [slots, Hv]: S before the chunk, FP32, in fragment order
   uint8_t* d_ws = nullptr;  // [slots, Hv]: the gradient of S after the chunk, likewise
-  uint8_t* w_ws = nullptr;  // [slots, Hv]: W, V/64 tiles hi then V/64 tiles lo
+  uint8_t* w_ws = nullptr;  // [slots, Hv]: W, V/64 tiles of each of the three parts
   uint8_t* x_ws = nullptr;  // [slots, Hv]: lo tiles of dX (dv holds hi)
   float* dots = nullptr;    // [slots, Hv, V/16, 2, 64]: each strip's share of b and dbeta
   const float* dstate_out = nullptr;
@@ -207,12 +225,12 @@ __device__ __forceinline__ float load_beta(const DeltaArgs& a, long long tok, in
 __device__ __forceinline__ float clamp_decay(float g) { return g < kMinLogDecay ? kMinLogDecay : g; }
 
 // Copies `live` rows of `cols` (a multiple of 64) BF16 values into swizzled tiles (one per 64
-// columns), zero below; all threads of the CTA take part.
+// columns), zero below; kThreads threads take part.
 template <int kThreads>
 __device__ __forceinline__ void load_rows(uint32_t dst, const uint16_t* src, long long ld, int cols,
-                                          int live) {
+                                          int live, int tid) {
   const int per = cols >> 3;
-  for (int i = threadIdx.x; i < kChunk * per; i += kThreads) {
+  for (int i = tid; i < kChunk * per; i += kThreads) {
     const int row = i / per, p = i - row * per;
     const bool ok = row < live;
     cp16(dst + (p >> 3) * kTileBytes + tile_off(row, p & 7), src + (ok ? row * ld : 0) + p * 8, ok);
@@ -220,8 +238,8 @@ __device__ __forceinline__ void load_rows(uint32_t dst, const uint16_t* src, lon
 }
 // Copies contiguous bytes (a multiple of 16).
 template <int kThreads>
-__device__ __forceinline__ void load_flat(uint32_t dst, const uint8_t* src, int bytes) {
-  for (int i = threadIdx.x * 16; i < bytes; i += kThreads * 16) cp16(dst + i, src + i, true);
+__device__ __forceinline__ void load_flat(uint32_t dst, const uint8_t* src, int bytes, int tid) {
+  for (int i = tid * 16; i < bytes; i += kThreads * 16) cp16(dst + i, src + i, true);
 }
 
 }  // namespace gnorm

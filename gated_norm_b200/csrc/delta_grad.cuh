@@ -69,8 +69,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
   const int i0 = mw * 16;
   const int ra = i0 + (lane >> 2), rb = ra + 8;
 
-  load_rows<kGradThreads>(s0 + L::kQ, a.q + t0 * a.ldq + static_cast<long long>(hk) * KD, a.ldq, KD, live);
-  load_rows<kGradThreads>(s0 + L::kK, a.k + t0 * a.ldk + static_cast<long long>(hk) * KD, a.ldk, KD, live);
+  load_rows<kGradThreads>(s0 + L::kQ, a.q + t0 * a.ldq + static_cast<long long>(hk) * KD, a.ldq, KD, live, tid);
+  load_rows<kGradThreads>(s0 + L::kK, a.k + t0 * a.ldk + static_cast<long long>(hk) * KD, a.ldk, KD, live, tid);
   float dq[kNT][4], dk[kNT][4];
 #pragma unroll
   for (int n = 0; n < kNT; ++n)
@@ -83,10 +83,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
     const long long hs = slot * a.Hv + h;
     const float4* S4 = reinterpret_cast<const float4*>(a.s_ws + hs * KD * VD * 4);
     const float4* D4 = reinterpret_cast<const float4*>(a.d_ws + hs * KD * VD * 4);
-    load_rows<kGradThreads>(s0 + L::kDo, a.dout + t0 * a.lddo + static_cast<long long>(h) * VD, a.lddo, VD, live);
-    load_rows<kGradThreads>(s0 + L::kXh, a.dv + t0 * a.lddv + static_cast<long long>(h) * VD, a.lddv, VD, live);
-    load_flat<kGradThreads>(s0 + L::kXl, a.x_ws + hs * (kVT * kTileBytes), kVT * kTileBytes);
-    load_flat<kGradThreads>(s0 + L::kW, a.w_ws + hs * (2 * kVT * kTileBytes), 2 * kVT * kTileBytes);
+    load_rows<kGradThreads>(s0 + L::kDo, a.dout + t0 * a.lddo + static_cast<long long>(h) * VD, a.lddo, VD, live, tid);
+    load_rows<kGradThreads>(s0 + L::kXh, a.dv + t0 * a.lddv + static_cast<long long>(h) * VD, a.lddv, VD, live, tid);
+    load_flat<kGradThreads>(s0 + L::kXl, a.x_ws + hs * (kVT * kTileBytes), kVT * kTileBytes, tid);
+    load_flat<kGradThreads>(s0 + L::kW, a.w_ws + hs * (3 * kVT * kTileBytes), 2 * kVT * kTileBytes, tid);
     cp_commit();
     // a state in fragment order -> hi and lo tiles [v][k]
     auto state_tiles = [&](const float4* src) {
@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
       Gs[ta] = s - static_cast<double>(gb);
       Gs[tb] = s;
     } else {
-      const float* ps = reinterpret_cast<const float*>(a.prep + hs * kPrepBytes + kPrepTiles);
+      const float* ps = reinterpret_cast<const float*>(a.prep + hs * kPrepBytes + kPrepTri);
       for (int i = tid - 32; i < 193; i += kGradThreads - 32) scal[i] = ps[i];
       // the strips' shares of b and dbeta, in strip order
       if (tid >= 128) {

@@ -16,17 +16,19 @@ constexpr int kPrepThreads = 128;
 constexpr int kKbLd = 68;  // floats of a row of Kb in shared memory
 
 template <int KD>
+GNORM_HD constexpr int prep_tile_area() {  // the q and k tiles, then the parts that go out
+  return KD / 64 * 2 * kTileBytes > kPrepTri ? KD / 64 * 2 * kTileBytes : static_cast<int>(kPrepTri);
+}
+template <int KD>
 GNORM_HD constexpr int prep_smem() {
-  // q and k tiles, reused for the tiles that go out; Kb; G; scalars
-  return (KD / 64 * 2 * kTileBytes > 4 * kTileBytes ? KD / 64 * 2 * kTileBytes : 4 * kTileBytes) +
-         64 * kKbLd * 4 + 64 * 8 + 1024;
+  return prep_tile_area<KD>() + 64 * kKbLd * 4 + 64 * 8 + 1024;  // Kb; G; scalars
 }
 
 template <int KD>
 __global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(const __grid_constant__ DeltaArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
   constexpr int kTiles = KD / 64;
-  constexpr int kTileArea = kTiles * 2 * kTileBytes > 4 * kTileBytes ? kTiles * 2 * kTileBytes : 4 * kTileBytes;
+  constexpr int kTileArea = prep_tile_area<KD>();
   float* kb = reinterpret_cast<float*>(smem + kTileArea);
   double* Gs = reinterpret_cast<double*>(kb + 64 * kKbLd);
   float* scal = reinterpret_cast<float*>(Gs + 64);  // beta, gamma, lambda [64], e^{G_C}
@@ -50,8 +52,8 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(const __gri
     return;
   }
   const uint32_t sq = smem_u32(smem), sk = sq + kTiles * kTileBytes;
-  load_rows<kPrepThreads>(sq, a.q + t0 * a.ldq + static_cast<long long>(hk) * KD, a.ldq, KD, live);
-  load_rows<kPrepThreads>(sk, a.k + t0 * a.ldk + static_cast<long long>(hk) * KD, a.ldk, KD, live);
+  load_rows<kPrepThreads>(sq, a.q + t0 * a.ldq + static_cast<long long>(hk) * KD, a.ldq, KD, live, tid);
+  load_rows<kPrepThreads>(sk, a.k + t0 * a.ldk + static_cast<long long>(hk) * KD, a.ldk, KD, live, tid);
   cp_commit();
   cp_wait<0>();
   __syncthreads();
@@ -85,7 +87,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(const __gri
   __syncthreads();  // the q and k tiles are free
 
   const int group = a.Hv / a.Hk;
-  uint8_t* tiles = smem;  // N hi, N lo, P hi, P lo
+  uint8_t* tiles = smem;  // N in three parts, P in three parts
   for (int r = 0; r < group; ++r) {
     const int h = hk * group + r;
     if (warp == 0) {
@@ -131,14 +133,17 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(const __gri
           make_float2(c < ra ? kk[n][0] * d[0] : 0.f, c + 1 < ra ? kk[n][1] * d[1] : 0.f);
       *reinterpret_cast<float2*>(kb + rb * kKbLd + c) =
           make_float2(c < rb ? kk[n][2] * d[2] : 0.f, c + 1 < rb ? kk[n][3] * d[3] : 0.f);
-      uint32_t hi, lo;
-      const uint32_t oa = tile_off(ra, n) + (c & 7) * 2, ob = tile_off(rb, n) + (c & 7) * 2;
-      split2(p[0], p[1], hi, lo);
-      *reinterpret_cast<uint32_t*>(tiles + 2 * kTileBytes + oa) = hi;
-      *reinterpret_cast<uint32_t*>(tiles + 3 * kTileBytes + oa) = lo;
-      split2(p[2], p[3], hi, lo);
-      *reinterpret_cast<uint32_t*>(tiles + 2 * kTileBytes + ob) = hi;
-      *reinterpret_cast<uint32_t*>(tiles + 3 * kTileBytes + ob) = lo;
+      if (n <= 2 * warp + 1) {
+        uint32_t pa[3], pb[3];
+        split3(p[0], p[1], pa);
+        split3(p[2], p[3], pb);
+        uint8_t* dst = tiles + 3 * kTriBytes;
+#pragma unroll
+        for (int part = 0; part < 3; ++part) {
+          *reinterpret_cast<uint32_t*>(dst + part * kTriBytes + tri_off(ra, c)) = pa[part];
+          *reinterpret_cast<uint32_t*>(dst + part * kTriBytes + tri_off(rb, c)) = pb[part];
+        }
+      }
     }
     __syncthreads();
     // forward substitution, column tid / 2; this thread keeps beta_l n_l of the blocks of
@@ -164,18 +169,28 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(const __gri
         s0 += __shfl_xor_sync(0xffffffffu, s0, 1);
         const float n = row[j] - s0;
         if (((i >> 2) & 1) == par) x[(i >> 3) * 4 + (i & 3)] = scal[i] * n;
-        const __nv_bfloat16 hi = __float2bfloat16_rn(n);
-        const __nv_bfloat16 out = par == 0 ? hi : __float2bfloat16_rn(n - __bfloat162float(hi));
-        *reinterpret_cast<__nv_bfloat16*>(tiles + par * kTileBytes + tile_off(i, j >> 3) +
-                                          (j & 7) * 2) = out;
+        // this thread's parts: the first, or the second and third
+        if ((j >> 4) <= (i >> 4)) {
+          const __nv_bfloat16 p0 = __float2bfloat16_rn(n);
+          uint8_t* dst = tiles + tri_off(i, j);
+          if (par == 0) {
+            *reinterpret_cast<__nv_bfloat16*>(dst) = p0;
+          } else {
+            const float r1 = n - __bfloat162float(p0);
+            const __nv_bfloat16 p1 = __float2bfloat16_rn(r1);
+            *reinterpret_cast<__nv_bfloat16*>(dst + kTriBytes) = p1;
+            *reinterpret_cast<__nv_bfloat16*>(dst + 2 * kTriBytes) =
+                __float2bfloat16_rn(r1 - __bfloat162float(p1));
+          }
+        }
       }
     }
     __syncthreads();
     uint8_t* dst = a.prep + (slot * a.Hv + h) * kPrepBytes;
-    for (int i = tid * 16; i < kPrepTiles; i += kPrepThreads * 16)
+    for (int i = tid * 16; i < kPrepTri; i += kPrepThreads * 16)
       *reinterpret_cast<uint4*>(dst + i) = *reinterpret_cast<const uint4*>(tiles + i);
     for (int i = tid; i < 193; i += kPrepThreads)
-      reinterpret_cast<float*>(dst + kPrepTiles)[i] = scal[i];
+      reinterpret_cast<float*>(dst + kPrepTri)[i] = scal[i];
     __syncthreads();
   }
 }

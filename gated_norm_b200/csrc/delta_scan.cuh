@@ -1,169 +1,309 @@
 // delta_scan.cuh -- the chunk-after-chunk part of the gated delta rule, forward and backward
 // (formulas and notation: delta_common.cuh).
 //
-// A warp owns 16 of the state's V columns for the whole sequence and keeps them, transposed,
-// as FP32 accumulators in registers (S^T: 16 x K).  Everything is computed transposed, so
-// each intermediate is the left operand of the next product and goes from accumulator to
-// operand layout inside the thread's registers: no shared-memory round trip, no barrier and
-// no other warp on the path from one chunk's state to the next.  The right operands (q, k, N,
-// P) are tiles in shared memory that all warps of the CTA read, double-buffered with
-// asynchronous copies.
+// Bound by the way from one chunk's state to the next, three small products in a row
+// (X = V - gamma K S, W = X - N beta X, S' = e^{G_C} S + K^T lambda Y) for every chunk of the
+// longest sequence.  So the work of a head is spread as widely as its products allow: a strip
+// of 16 of the state's V columns (an instruction's 16 rows, everything being computed
+// transposed) belongs to a group of four warps, one per scheduler of the SM, and a head of
+// 128 columns to eight strips on up to eight SMs.  Within a strip a warp owns a quarter of
+// the state's K columns, in registers for the whole sequence, and two of the chunk's eight
+// token tiles, w and 7 - w, whose shares of a triangular product add up to the same for every
+// warp.  Each intermediate goes from accumulators to the other warps as ready left operands
+// through shared memory, one barrier of the group per product.  Four more warps per strip, one
+// beside each of the others on its scheduler, take what the way from state to state does not
+// need: the copies of the right operands (q, k, N, P tiles, double-buffered), in the forward
+// the output, in the backward the terms of dO.
+//
+// The tensor cores of the fifth generation take at least 64 rows an instruction: a head's 128
+// columns would be one tile on one SM, its 66000 values a chunk would be cut and scaled by
+// that SM alone, and the other SMs would wait -- the heads of a layer are fewer than the SMs.
 #pragma once
 
 #include "delta_common.cuh"
 
 namespace gnorm {
 
-constexpr int kScanWarps = 4;  // 64 columns of V per CTA
-constexpr int kScanThreads = kScanWarps * 32;
+constexpr int kGroupThreads = 128;  // four warps on the state of a strip of 16 columns ...
+constexpr int kStripThreads = 256;  // ... and four beside them
 
-template <int KD, bool kBwd>
+// Named barriers of a strip: among its state warps, among the others, and from one to the other
+// (bar.arrive on one side, bar.sync on the other).
+enum { kBarState = 1, kBarSide = 2, kBarA = 3, kBarB = 4, kBarsPerStrip = 4 };
+__device__ __forceinline__ void bar_arrive(int id, int nthreads) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
+}
+
+// Strips of `G` groups, as 8 x 8 matrices [piece of 8 columns][tile of 8 tokens].
+template <int G>
+GNORM_HD constexpr int strip_bytes() { return G * 2048; }
+__device__ __forceinline__ uint32_t strip_off(int piece, int token) {
+  return static_cast<uint32_t>(((piece * 8 + (token >> 3)) * 8 + (token & 7)) * 16);
+}
+
+// Shared memory of a CTA: two stages, then each group's exchange buffers.
+template <int KD, int G, bool kBwd>
 struct ScanStage {
   static constexpr int kQ = 0;
   static constexpr int kK = KD / 64 * kTileBytes;
-  static constexpr int kN = 2 * kK;  // N hi, N lo, P hi, P lo, scalars
-  static constexpr int kScal = kN + 4 * kTileBytes;
-  static constexpr int kV = kScal + 1024;  // v (forward) or do (backward)
-  static constexpr int kW = kV + kTileBytes;  // W hi, W lo (backward)
-  static constexpr int kBytes = kBwd ? kW + 2 * kTileBytes : kW;
+  static constexpr int kTri = 2 * kK;  // N, then P (three parts each)
+  static constexpr int kScal = kTri + 6 * kTriBytes;
+  static constexpr int kV = kScal + 1024;               // v (forward) or do (backward)
+  static constexpr int kW = kV + strip_bytes<G>();      // W's three parts (backward)
+  static constexpr int kBytes = kW + (kBwd ? 3 * strip_bytes<G>() : 0);
 };
+constexpr int kFragBytes = 512;  // left operand of one 16 x 16 block, one part
+template <int KD, bool kBwd>
+struct ScanExchange {
+  static constexpr int kState = KD / 16 * 3 * kFragBytes;
+  static constexpr int kS = 0;  // the state, three parts; twice in the forward
+  static constexpr int kX = (kBwd ? 1 : 2) * kState;      // beta X (beta dY)
+  static constexpr int kY = kX + 12 * kFragBytes;         // lambda Y (gamma dX)
+  static constexpr int kO = kY + 12 * kFragBytes;         // Y, two parts (scale gamma dO, three)
+  static constexpr int kP = kO + (kBwd ? 12 : 8) * kFragBytes;  // scale P^T dO, FP32
+  static constexpr int kR = kP + (kBwd ? 4096 : 0);             // Q^T (scale gamma dO), FP32
+  static constexpr int kBytes = kR + (kBwd ? KD * 64 : 0);
+};
+template <int KD, int G, bool kBwd>
+GNORM_HD constexpr int scan_smem() {
+  return 2 * ScanStage<KD, G, kBwd>::kBytes + G * ScanExchange<KD, kBwd>::kBytes;
+}
 
 // Fragment order of a 16 x K strip of FP32 values: tile n (8 columns), lane, four values.
 __device__ __forceinline__ long long frag_off(int KD, int strip, int n, int lane) {
   return ((static_cast<long long>(strip) * (KD / 8) + n) * 32 + lane) * 16;
 }
 
-// acc (16 x 64 tokens) += A (16 x 16 at k16 block, hi and lo) times the transposed rows of
-// the 64-row tile at columns c0: an exact right operand.
-__device__ __forceinline__ void mul_rows_exact(float acc[8][4], const uint32_t hi[4],
-                                               const uint32_t lo[4], uint32_t tile, int c0,
-                                               int lane) {
+__device__ __forceinline__ void lds4(uint32_t r[4], uint32_t addr) {
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void sts2(uint32_t addr, uint32_t a, uint32_t b) {
+  asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
+
+// What a warp needs to know of its place: its token tiles and lane addresses.
+struct ScanLane {
+  int warp, lane;
+  __device__ __forceinline__ ScanLane(int w, int l) : warp(w), lane(l) {}
+  __device__ __forceinline__ int tile(int i) const { return i == 0 ? warp : 7 - warp; }
+  // token of column e (0, 1) of this lane in own tile i
+  __device__ __forceinline__ int token(int i) const { return tile(i) * 8 + 2 * (lane & 3); }
+  // right operand: rows are the own tokens of a [64, KD] tile
+  __device__ __forceinline__ uint32_t rows(uint32_t t, int col0) const {
+    const int row = tile(lane >> 4) * 8 + (lane & 7);
+    return t + tile_off(row, (col0 >> 3) + ((lane >> 3) & 1));
+  }
+  // the own tokens of a strip (its columns at `piece`)
+  __device__ __forceinline__ uint32_t strip(uint32_t s, int piece) const {
+    return s + strip_off(piece + ((lane >> 3) & 1), tile(lane >> 4) * 8 + (lane & 7));
+  }
+  // 16-byte piece `lane & 1` of own token `lane / 2`
+  __device__ __forceinline__ int row() const { return tile(lane >> 4) * 8 + ((lane >> 1) & 7); }
+};
+
+// Writes an own token tile (accumulator layout, scaled by f) as left operand parts.
+template <int kParts>
+__device__ __forceinline__ void put_tile(uint32_t buf, int tile, int lane, const float x[4]) {
+  uint32_t a[3], b[3];
+  if constexpr (kParts == 3) {
+    split3(x[0], x[1], a);
+    split3(x[2], x[3], b);
+  } else {
+    split2(x[0], x[1], a[0], a[1]);
+    split2(x[2], x[3], b[0], b[1]);
+  }
 #pragma unroll
-  for (int nb = 0; nb < 4; ++nb) {
+  for (int p = 0; p < kParts; ++p)
+    sts2(buf + ((tile >> 1) * kParts + p) * kFragBytes + lane * 16 + (tile & 1) * 8, a[p], b[p]);
+}
+
+// The warp's part of the state (columns n0 * 8 ..) as left operand, three parts.
+template <int KD>
+__device__ __forceinline__ void put_state(uint32_t buf, int warp, int lane,
+                                          const float st[KD / 32][4]) {
+#pragma unroll
+  for (int kb = 0; kb < KD / 64; ++kb) {
+    uint32_t f[4][3];
+    split3(st[2 * kb][0], st[2 * kb][1], f[0]);
+    split3(st[2 * kb][2], st[2 * kb][3], f[1]);
+    split3(st[2 * kb + 1][0], st[2 * kb + 1][1], f[2]);
+    split3(st[2 * kb + 1][2], st[2 * kb + 1][3], f[3]);
+#pragma unroll
+    for (int p = 0; p < 3; ++p)
+      asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(
+                       buf + ((warp * (KD / 64) + kb) * 3 + p) * kFragBytes + lane * 16),
+                   "r"(f[0][p]), "r"(f[1][p]), "r"(f[2][p]), "r"(f[3][p])
+                   : "memory");
+  }
+}
+
+// D = A B.
+__device__ __forceinline__ void mma16816_0(float d[4], const uint32_t a[4], uint32_t b0,
+                                           uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+__device__ __forceinline__ void zero_tiles(float x[2][4]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[i][e] = 0.f;
+}
+
+// acc (own tokens) = state (kParts of its three parts) times the rows of a [64, KD] tensor.
+template <int KD, int kParts>
+__device__ __forceinline__ void state_product(float acc[2][4], uint32_t sbuf, uint32_t tiles,
+                                              const ScanLane& me) {
+  float x[kParts][2][4];
+#pragma unroll
+  for (int kb = 0; kb < KD / 16; ++kb) {
     uint32_t b[4];
-    ldsm4(b, addr_b(tile, nb * 16, c0, lane));
-    mma16816(acc[2 * nb], hi, b[0], b[1]);
-    mma16816(acc[2 * nb + 1], hi, b[2], b[3]);
-    mma16816(acc[2 * nb], lo, b[0], b[1]);
-    mma16816(acc[2 * nb + 1], lo, b[2], b[3]);
-  }
-}
-
-// acc (16 x 64) += A (16 x 64, split) M^T for a lower triangular 64 x 64 M given as hi and lo
-// tiles: column block nb takes the k blocks up to nb.
-__device__ __forceinline__ void mul_lower_t(float acc[8][4], const uint32_t (*hi)[4],
-                                            const uint32_t (*lo)[4], uint32_t mhi, uint32_t mlo,
-                                            int lane) {
+    ldsm4(b, me.rows(tiles + (kb >> 2) * kTileBytes, (kb & 3) * 16));
 #pragma unroll
-  for (int nb = 0; nb < 4; ++nb) {
-#pragma unroll
-    for (int kb = 0; kb <= nb; ++kb) {
-      uint32_t b[4], c[4];
-      ldsm4(b, addr_b(mhi, nb * 16, kb * 16, lane));
-      ldsm4(c, addr_b(mlo, nb * 16, kb * 16, lane));
-      mma16816(acc[2 * nb], hi[kb], b[0], b[1]);
-      mma16816(acc[2 * nb + 1], hi[kb], b[2], b[3]);
-      mma16816(acc[2 * nb], lo[kb], b[0], b[1]);
-      mma16816(acc[2 * nb + 1], lo[kb], b[2], b[3]);
-      mma16816(acc[2 * nb], hi[kb], c[0], c[1]);
-      mma16816(acc[2 * nb + 1], hi[kb], c[2], c[3]);
-    }
-  }
-}
-
-// The same against M itself (k are M's rows): column block nb takes the k blocks from nb on.
-// kExact: A is exact (lo unused).
-template <bool kExact>
-__device__ __forceinline__ void mul_lower(float acc[8][4], const uint32_t (*hi)[4],
-                                          const uint32_t (*lo)[4], uint32_t mhi, uint32_t mlo,
-                                          int lane) {
-#pragma unroll
-  for (int nb = 0; nb < 4; ++nb) {
-#pragma unroll
-    for (int kb = nb; kb < 4; ++kb) {
-      uint32_t b[4], c[4];
-      ldsm4t(b, addr_bt(mhi, kb * 16, nb * 16, lane));
-      ldsm4t(c, addr_bt(mlo, kb * 16, nb * 16, lane));
-      mma16816(acc[2 * nb], hi[kb], b[0], b[1]);
-      mma16816(acc[2 * nb + 1], hi[kb], b[2], b[3]);
-      if constexpr (!kExact) {
-        mma16816(acc[2 * nb], lo[kb], b[0], b[1]);
-        mma16816(acc[2 * nb + 1], lo[kb], b[2], b[3]);
+    for (int p = 0; p < kParts; ++p) {
+      uint32_t a[4];
+      lds4(a, sbuf + (kb * 3 + p) * kFragBytes + me.lane * 16);
+      if (kb == 0) {
+        mma16816_0(x[p][0], a, b[0], b[1]);
+        mma16816_0(x[p][1], a, b[2], b[3]);
+      } else {
+        mma16816(x[p][0], a, b[0], b[1]);
+        mma16816(x[p][1], a, b[2], b[3]);
       }
-      mma16816(acc[2 * nb], hi[kb], c[0], c[1]);
-      mma16816(acc[2 * nb + 1], hi[kb], c[2], c[3]);
     }
   }
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      acc[i][e] = x[kParts - 1][i][e];
+#pragma unroll
+      for (int p = kParts - 2; p >= 0; --p) acc[i][e] += x[p][i][e];
+    }
 }
 
-// S^T (16 x KD) += A (16 x 64 tokens, split) times the rows of a [64, KD] tensor (exact).
-template <int KD>
-__device__ __forceinline__ void rank_update(float st[KD / 8][4], const uint32_t (*hi)[4],
-                                            const uint32_t (*lo)[4], uint32_t tiles, int lane) {
+// acc (own tokens) += A (16 x 64 tokens, kA parts in `abuf`) times the lower triangular M
+// (kM parts): kTrans = false: sum over j <= i of A_j M_ij, own tokens i; true: sum over i >= j
+// of A_i M_ij, own tokens j.  Products of parts a + m < kOrder are taken, each order in sums
+// of its own.
+template <bool kTrans, int kA, int kM, int kOrder>
+__device__ __forceinline__ void tri_product(float acc[2][4], const uint32_t* exact, uint32_t abuf,
+                                            uint32_t tri, const ScanLane& me) {
+  float x[kOrder][2][4];
+#pragma unroll
+  for (int o = 0; o < kOrder; ++o) zero_tiles(x[o]);
 #pragma unroll
   for (int kb = 0; kb < 4; ++kb) {
+    const bool use0 = kTrans ? kb >= me.tile(0) >> 1 : kb <= me.tile(0) >> 1;
+    const bool use1 = kTrans ? kb >= me.tile(1) >> 1 : kb <= me.tile(1) >> 1;
+    if (use0 || use1) {
+      // a tile that takes no part reads the other's matrices
+      const int t = (me.lane >> 4) ? (use1 ? me.tile(1) : me.tile(0)) : (use0 ? me.tile(0) : me.tile(1));
+      const int hf = (me.lane >> 3) & 1;
+      const int m = kTrans ? tri_row(2 * kb + hf) + t : tri_row(t) + 2 * kb + hf;
+      const uint32_t addr = tri + m * 128 + (me.lane & 7) * 16;
+      uint32_t b[kM][4];
 #pragma unroll
-    for (int nb = 0; nb < KD / 16; ++nb) {
-      uint32_t b[4];
-      ldsm4t(b, addr_bt(tiles + (nb >> 2) * kTileBytes, kb * 16, (nb & 3) * 16, lane));
-      mma16816(st[2 * nb], hi[kb], b[0], b[1]);
-      mma16816(st[2 * nb + 1], hi[kb], b[2], b[3]);
-      mma16816(st[2 * nb], lo[kb], b[0], b[1]);
-      mma16816(st[2 * nb + 1], lo[kb], b[2], b[3]);
+      for (int p = 0; p < kM; ++p) {
+        if constexpr (kTrans)
+          ldsm4t(b[p], addr + p * kTriBytes);
+        else
+          ldsm4(b[p], addr + p * kTriBytes);
+      }
+#pragma unroll
+      for (int q = 0; q < kA; ++q) {
+        uint32_t a[4];
+        if (exact != nullptr) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) a[e] = exact[kb * 4 + e];
+        } else {
+          lds4(a, abuf + (kb * kA + q) * kFragBytes + me.lane * 16);
+        }
+#pragma unroll
+        for (int p = 0; p < kM; ++p) {
+          if (q + p < kOrder) {
+            if (use0) mma16816(x[q + p][0], a, b[p][0], b[p][1]);
+            if (use1) mma16816(x[q + p][1], a, b[p][2], b[p][3]);
+          }
+        }
+      }
     }
   }
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float v = x[kOrder - 1][i][e];
+#pragma unroll
+      for (int o = kOrder - 2; o >= 0; --o) v += x[o][i][e];
+      acc[i][e] += v;
+    }
 }
 
-// x (16 x 64 tokens, accumulator layout) times f[token], as split fragments.
-__device__ __forceinline__ void split_scaled(const float x[8][4], const float* f, float s,
-                                             uint32_t (*hi)[4], uint32_t (*lo)[4], int lane) {
+// The warp's part of S^T += A (16 x 64 tokens, three parts) times the rows of a [64, KD] tensor;
+// kNeg: -=.
+template <int KD, bool kNeg>
+__device__ __forceinline__ void rank_update(float st[KD / 32][4], uint32_t abuf, uint32_t tiles,
+                                            const ScanLane& me) {
+  constexpr int kNB = KD / 64;
 #pragma unroll
   for (int kb = 0; kb < 4; ++kb) {
-    float t[2][4];
+    uint32_t b[kNB][4];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const float2 w = *reinterpret_cast<const float2*>(f + (2 * kb + u) * 8 + 2 * (lane & 3));
-      t[u][0] = x[2 * kb + u][0] * (w.x * s);
-      t[u][1] = x[2 * kb + u][1] * (w.y * s);
-      t[u][2] = x[2 * kb + u][2] * (w.x * s);
-      t[u][3] = x[2 * kb + u][3] * (w.y * s);
+    for (int nb = 0; nb < kNB; ++nb) {
+      const int col = (me.warp * kNB + nb) * 16;
+      ldsm4t(b[nb], addr_bt(tiles + (col >> 6) * kTileBytes, kb * 16, col & 63, me.lane));
     }
-    split_frag(t[0], t[1], hi[kb], lo[kb]);
-  }
-}
-
-// The strip's 16 columns of a [64 tokens, 64] tile in shared memory, as packed pairs in the
-// accumulator layout of its transpose: r[n][0] rows lane/4, r[n][1] rows lane/4 + 8.
-__device__ __forceinline__ void load_strip(uint32_t r[8][2], uint32_t tile, int col0, int lane) {
 #pragma unroll
-  for (int tb = 0; tb < 4; ++tb) {
-    uint32_t f[4];
-    ldsm4t(f, addr_at(tile, tb * 16, col0, lane));
-    r[2 * tb][0] = f[0];
-    r[2 * tb][1] = f[1];
-    r[2 * tb + 1][0] = f[2];
-    r[2 * tb + 1][1] = f[3];
-  }
-}
-
-// The other way: pairs into the strip's columns of the tile, then 16-byte stores of its rows.
-__device__ __forceinline__ void stage_strip(const uint32_t r[8][2], uint32_t tile, int col0,
-                                            int lane) {
+    for (int p = 0; p < 3; ++p) {
+      uint32_t a[4];
+      lds4(a, abuf + (kb * 3 + p) * kFragBytes + me.lane * 16);
+      if constexpr (kNeg) {
 #pragma unroll
-  for (int tb = 0; tb < 4; ++tb) {
-    const uint32_t f[4] = {r[2 * tb][0], r[2 * tb][1], r[2 * tb + 1][0], r[2 * tb + 1][1]};
-    stsm4t(addr_at(tile, tb * 16, col0, lane), f);
+        for (int e = 0; e < 4; ++e) a[e] ^= 0x80008000u;
+      }
+#pragma unroll
+      for (int nb = 0; nb < kNB; ++nb) {
+        mma16816(st[2 * nb], a, b[nb][0], b[nb][1]);
+        mma16816(st[2 * nb + 1], a, b[nb][2], b[nb][3]);
+      }
+    }
   }
 }
 
+// Copies `live` rows of 2 G pieces into strip matrices, zero below.
+template <int kThreads, int G>
+__device__ __forceinline__ void load_strips(uint32_t dst, const uint16_t* src, long long ld,
+                                            int live, int tid) {
+  for (int i = tid; i < kChunk * 2 * G; i += kThreads) {
+    const int row = i / (2 * G), p = i - row * 2 * G;
+    const bool ok = row < live;
+    cp16(dst + strip_off(p, row), src + (ok ? row * ld : 0) + p * 8, ok);
+  }
+}
+// The same from a swizzled 64 x 64 tile, its columns from `piece` on.
+template <int kThreads, int G>
+__device__ __forceinline__ void load_strips_tile(uint32_t dst, const uint8_t* tile, int piece,
+                                                 int tid) {
+  for (int i = tid; i < kChunk * 2 * G; i += kThreads) {
+    const int row = i / (2 * G), p = i - row * 2 * G;
+    cp16(dst + strip_off(p, row), tile + tile_off(row, piece + p), true);
+  }
+}
+
+// The warp's part of a state [KD, V], transposed.
 template <int KD>
-__device__ __forceinline__ void load_state(float st[KD / 8][4], const float* p, int V, int v0,
-                                           int lane) {
-  // p: [KD, V] of this (sequence, head); st: the transposed strip
-  const int va = v0 + (lane >> 2);
+__device__ __forceinline__ void load_state(float st[KD / 32][4], const float* p, int V, int v0,
+                                           const ScanLane& me) {
+  const int va = v0 + (me.lane >> 2);
 #pragma unroll
-  for (int n = 0; n < KD / 8; ++n) {
-    const int k0 = n * 8 + 2 * (lane & 3);
+  for (int n = 0; n < KD / 32; ++n) {
+    const int k0 = (me.warp * (KD / 32) + n) * 8 + 2 * (me.lane & 3);
     st[n][0] = p[static_cast<long long>(k0) * V + va];
     st[n][1] = p[static_cast<long long>(k0 + 1) * V + va];
     st[n][2] = p[static_cast<long long>(k0) * V + va + 8];
@@ -171,12 +311,12 @@ __device__ __forceinline__ void load_state(float st[KD / 8][4], const float* p, 
   }
 }
 template <int KD>
-__device__ __forceinline__ void store_state(const float st[KD / 8][4], float* p, int V, int v0,
-                                            int lane) {
-  const int va = v0 + (lane >> 2);
+__device__ __forceinline__ void store_state(const float st[KD / 32][4], float* p, int V, int v0,
+                                            const ScanLane& me) {
+  const int va = v0 + (me.lane >> 2);
 #pragma unroll
-  for (int n = 0; n < KD / 8; ++n) {
-    const int k0 = n * 8 + 2 * (lane & 3);
+  for (int n = 0; n < KD / 32; ++n) {
+    const int k0 = (me.warp * (KD / 32) + n) * 8 + 2 * (me.lane & 3);
     p[static_cast<long long>(k0) * V + va] = st[n][0];
     p[static_cast<long long>(k0 + 1) * V + va] = st[n][1];
     p[static_cast<long long>(k0) * V + va + 8] = st[n][2];
@@ -184,250 +324,330 @@ __device__ __forceinline__ void store_state(const float st[KD / 8][4], float* p,
   }
 }
 
+// Own tokens of a strip in shared memory as FP32 in accumulator layout.
+__device__ __forceinline__ void get_strip(float x[2][4], uint32_t strip, int piece,
+                                          const ScanLane& me) {
+  uint32_t f[4];
+  ldsm4t(f, me.strip(strip, piece));
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    x[i][0] = bf_lo(f[2 * i]);
+    x[i][1] = bf_hi(f[2 * i]);
+    x[i][2] = bf_lo(f[2 * i + 1]);
+    x[i][3] = bf_hi(f[2 * i + 1]);
+  }
+}
+
+// Own tokens as BF16 pairs through the strip matrices (this warp's alone): the 16 bytes of
+// token me.row(), piece lane & 1.
+__device__ __forceinline__ uint4 turn_strip(const uint32_t f[4], uint32_t strip, uint8_t* generic,
+                                            int piece, const ScanLane& me) {
+  __syncwarp();
+  stsm4t(me.strip(strip, piece), f);
+  __syncwarp();
+  return *reinterpret_cast<const uint4*>(generic + strip_off(piece + (me.lane & 1), me.row()));
+}
+
 // Forward.  kOut: writes o and the final state.  kSave: writes every chunk's S and W for the
 // backward (which runs this pass again instead of keeping them since the forward).
-template <int KD, bool kOut, bool kSave>
-__global__ void __launch_bounds__(kScanThreads, 1) delta_scan_fwd_kernel(const __grid_constant__ DeltaArgs a) {
-  using St = ScanStage<KD, false>;
+template <int KD, int G, bool kOut, bool kSave>
+__global__ void __launch_bounds__(G * kStripThreads, 1)
+    delta_scan_fwd_kernel(const __grid_constant__ DeltaArgs a) {
+  using St = ScanStage<KD, G, false>;
+  using Ex = ScanExchange<KD, false>;
+  constexpr int kLoaders = G * kGroupThreads;
   extern __shared__ __align__(128) uint8_t smem[];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int vt = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+  const int group = threadIdx.x / kStripThreads;
+  const bool side = (threadIdx.x & kGroupThreads) != 0;
+  const ScanLane me((threadIdx.x >> 5) & 3, threadIdx.x & 31);
+  const int lane = me.lane;
+  const int bars = group * kBarsPerStrip;
+  const int h = blockIdx.y, b = blockIdx.z;
   const int hk = h / (a.Hv / a.Hk);
-  const int col0 = warp * 16, v0 = vt * 64 + col0, strip = v0 / 16;
+  const int vc = blockIdx.x * 16 * G;  // the CTA's first column
+  const int v0 = vc + group * 16, strip = v0 / 16;
   grid_dependency_wait();
   allow_dependent_launch();
   const long long start = seq_start(a.seq, b), end = seq_end(a.seq, b);
   const long long base = seq_base(a.seq, b);
   const int chunks = static_cast<int>((end - start + kChunk - 1) / kChunk);
   const uint32_t sbase = smem_u32(smem);
+  const uint32_t ex = sbase + 2 * St::kBytes + group * Ex::kBytes;
 
-  auto issue = [&](int c) {
-    const uint32_t st = sbase + (c & 1) * St::kBytes;
-    const long long t0 = start + static_cast<long long>(c) * kChunk;
-    const int live = static_cast<int>(end - t0 < kChunk ? end - t0 : kChunk);
-    if constexpr (kOut)
-      load_rows<kScanThreads>(st + St::kQ, a.q + t0 * a.ldq + static_cast<long long>(hk) * KD, a.ldq,
-                              KD, live);
-    load_rows<kScanThreads>(st + St::kK, a.k + t0 * a.ldk + static_cast<long long>(hk) * KD, a.ldk,
-                            KD, live);
-    const uint8_t* prep = a.prep + ((base + c) * a.Hv + h) * kPrepBytes;
-    load_flat<kScanThreads>(st + St::kN, prep, kOut ? 4 * kTileBytes : 2 * kTileBytes);
-    load_flat<kScanThreads>(st + St::kScal, prep + kPrepTiles, 784);
-    load_rows<kScanThreads>(st + St::kV, a.v + t0 * a.ldv + static_cast<long long>(h) * a.V + vt * 64,
-                            a.ldv, 64, live);
-    cp_commit();
-  };
+  if (side) {
+    const int tid = group * kGroupThreads + (threadIdx.x & (kGroupThreads - 1));
+    auto issue = [&](int c) {
+      const uint32_t st = sbase + (c & 1) * St::kBytes;
+      const long long t0 = start + static_cast<long long>(c) * kChunk;
+      const int live = static_cast<int>(end - t0 < kChunk ? end - t0 : kChunk);
+      load_rows<kLoaders>(st + St::kK, a.k + t0 * a.ldk + static_cast<long long>(hk) * KD, a.ldk, KD,
+                          live, tid);
+      const uint8_t* prep = a.prep + ((base + c) * a.Hv + h) * kPrepBytes;
+      load_flat<kLoaders>(st + St::kTri, prep, (kOut ? 5 : 3) * kTriBytes, tid);
+      load_flat<kLoaders>(st + St::kScal, prep + kPrepTri, 784, tid);
+      load_strips<kLoaders, G>(st + St::kV, a.v + t0 * a.ldv + static_cast<long long>(h) * a.V + vc,
+                               a.ldv, live, tid);
+      if constexpr (kOut)
+        load_rows<kLoaders>(st + St::kQ, a.q + t0 * a.ldq + static_cast<long long>(hk) * KD, a.ldq,
+                            KD, live, tid);
+      cp_commit();
+    };
+    if (chunks > 0) issue(0);
+    for (int c = 0; c < chunks; ++c) {
+      cp_wait<0>();
+      __syncthreads();  // stage c has arrived, the other one is free, the state can be read
+      if (c + 1 < chunks) issue(c + 1);
+      if constexpr (kOut) {
+        uint8_t* stage = smem + (c & 1) * St::kBytes;
+        const uint32_t sg = sbase + (c & 1) * St::kBytes;
+        const float* scal = reinterpret_cast<const float*>(stage + St::kScal);
+        const long long t0 = start + static_cast<long long>(c) * kChunk;
+        const int live = static_cast<int>(end - t0 < kChunk ? end - t0 : kChunk);
+        // O = scale (gamma Q S + P Y)
+        float o[2][4];
+        state_product<KD, 2>(o, ex + Ex::kS + (c & 1) * Ex::kState, sg + St::kQ, me);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float2 gm = *reinterpret_cast<const float2*>(scal + 64 + me.token(i));
+          o[i][0] *= gm.x;
+          o[i][1] *= gm.y;
+          o[i][2] *= gm.x;
+          o[i][3] *= gm.y;
+        }
+        named_barrier_sync(bars + kBarA, kStripThreads);  // Y can be read
+        tri_product<false, 2, 2, 2>(o, nullptr, ex + Ex::kO, sg + St::kTri + 3 * kTriBytes, me);
+        uint32_t f[4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          f[2 * i] = pack_bf16x2(a.scale * o[i][0], a.scale * o[i][1]);
+          f[2 * i + 1] = pack_bf16x2(a.scale * o[i][2], a.scale * o[i][3]);
+        }
+        const uint4 v = turn_strip(f, sg + St::kV, stage + St::kV, group * 2, me);
+        const int row = me.row();
+        if (row < live)
+          *reinterpret_cast<uint4*>(a.o + (t0 + row) * a.ldo + static_cast<long long>(h) * a.V + v0 +
+                                    (lane & 1) * 8) = v;
+      }
+    }
+    return;
+  }
 
-  float st[KD / 8][4];
+  float st[KD / 32][4];
   const long long head_state = (static_cast<long long>(b) * a.Hv + h) * KD * a.V;
   if (a.state_in != nullptr) {
-    load_state<KD>(st, a.state_in + head_state, a.V, v0, lane);
+    load_state<KD>(st, a.state_in + head_state, a.V, v0, me);
   } else {
 #pragma unroll
-    for (int n = 0; n < KD / 8; ++n)
+    for (int n = 0; n < KD / 32; ++n)
 #pragma unroll
       for (int e = 0; e < 4; ++e) st[n][e] = 0.f;
   }
-  if (chunks > 0) issue(0);
   for (int c = 0; c < chunks; ++c) {
-    if (c + 1 < chunks) {
-      issue(c + 1);
-      cp_wait<1>();
-    } else {
-      cp_wait<0>();
-    }
+    const uint32_t sbuf = ex + Ex::kS + (c & 1) * Ex::kState;
+    put_state<KD>(sbuf, me.warp, lane, st);
     __syncthreads();
+    uint8_t* stage = smem + (c & 1) * St::kBytes;
     const uint32_t sg = sbase + (c & 1) * St::kBytes;
-    const float* scal = reinterpret_cast<const float*>(smem + (c & 1) * St::kBytes + St::kScal);
-    const long long t0 = start + static_cast<long long>(c) * kChunk;
-    const int live = static_cast<int>(end - t0 < kChunk ? end - t0 : kChunk);
+    const float* scal = reinterpret_cast<const float*>(stage + St::kScal);
     const long long hs = (base + c) * a.Hv + h;
+    // X = V - gamma K S
+    float x[2][4], y[2][4];
+    state_product<KD, 3>(x, sbuf, sg + St::kK, me);
+    get_strip(y, sg + St::kV, group * 2, me);
+    float2 be[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float2 gm = *reinterpret_cast<const float2*>(scal + 64 + me.token(i));
+      be[i] = *reinterpret_cast<const float2*>(scal + me.token(i));
+      x[i][0] = fmaf(-gm.x, x[i][0], y[i][0]);
+      x[i][1] = fmaf(-gm.y, x[i][1], y[i][1]);
+      x[i][2] = fmaf(-gm.x, x[i][2], y[i][2]);
+      x[i][3] = fmaf(-gm.y, x[i][3], y[i][3]);
+      // the sign of W = X - N (beta X) is in the operand
+      const float t[4] = {-be[i].x * x[i][0], -be[i].y * x[i][1], -be[i].x * x[i][2],
+                          -be[i].y * x[i][3]};
+      put_tile<3>(ex + Ex::kX, me.tile(i), lane, t);
+    }
+    named_barrier_sync(bars + kBarState, kGroupThreads);
+    tri_product<false, 3, 3, 3>(x, nullptr, ex + Ex::kX, sg + St::kTri, me);
+    // Y = beta W
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float2 lm = *reinterpret_cast<const float2*>(scal + 128 + me.token(i));
+      y[i][0] = be[i].x * x[i][0];
+      y[i][1] = be[i].y * x[i][1];
+      y[i][2] = be[i].x * x[i][2];
+      y[i][3] = be[i].y * x[i][3];
+      if constexpr (kOut) put_tile<2>(ex + Ex::kO, me.tile(i), lane, y[i]);
+      y[i][0] *= lm.x;
+      y[i][1] *= lm.y;
+      y[i][2] *= lm.x;
+      y[i][3] *= lm.y;
+      put_tile<3>(ex + Ex::kY, me.tile(i), lane, y[i]);
+    }
+    if constexpr (kOut) bar_arrive(bars + kBarA, kStripThreads);
     if constexpr (kSave) {
       uint8_t* p = a.s_ws + hs * KD * a.V * 4;
 #pragma unroll
-      for (int n = 0; n < KD / 8; ++n)
-        *reinterpret_cast<float4*>(p + frag_off(KD, strip, n, lane)) =
+      for (int n = 0; n < KD / 32; ++n)
+        *reinterpret_cast<float4*>(p + frag_off(KD, strip, me.warp * (KD / 32) + n, lane)) =
             make_float4(st[n][0], st[n][1], st[n][2], st[n][3]);
     }
-    // S^T K^T and S^T Q^T
-    float x[8][4], o[8][4];
-#pragma unroll
-    for (int n = 0; n < 8; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[n][e] = o[n][e] = 0.f;
-#pragma unroll
-    for (int kb = 0; kb < KD / 16; ++kb) {
-      uint32_t hi[4], lo[4];
-      split_frag(st[2 * kb], st[2 * kb + 1], hi, lo);
-      const uint32_t toff = (kb >> 2) * kTileBytes;
-      mul_rows_exact(x, hi, lo, sg + St::kK + toff, (kb & 3) * 16, lane);
-      if constexpr (kOut) mul_rows_exact(o, hi, lo, sg + St::kQ + toff, (kb & 3) * 16, lane);
-    }
-    // X = V - gamma K S
-    {
-      uint32_t vv[8][2];
-      load_strip(vv, sg + St::kV, col0, lane);
-#pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        const float2 gm = *reinterpret_cast<const float2*>(scal + 64 + n * 8 + 2 * (lane & 3));
-        x[n][0] = fmaf(-gm.x, x[n][0], bf_lo(vv[n][0]));
-        x[n][1] = fmaf(-gm.y, x[n][1], bf_hi(vv[n][0]));
-        x[n][2] = fmaf(-gm.x, x[n][2], bf_lo(vv[n][1]));
-        x[n][3] = fmaf(-gm.y, x[n][3], bf_hi(vv[n][1]));
-        o[n][0] *= gm.x;
-        o[n][1] *= gm.y;
-        o[n][2] *= gm.x;
-        o[n][3] *= gm.y;
-      }
-    }
-    uint32_t hi[4][4], lo[4][4];
-    // W = X - N (beta X): with the sign in the operand
-    split_scaled(x, scal, -1.f, hi, lo, lane);
-    mul_lower_t(x, hi, lo, sg + St::kN, sg + St::kN + kTileBytes, lane);
-    if constexpr (kSave) {
-      // W as hi and lo tiles, through the strip's columns of the v tile (this warp's alone)
-      uint32_t wh[8][2], wl[8][2];
-#pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        split2(x[n][0], x[n][1], wh[n][0], wl[n][0]);
-        split2(x[n][2], x[n][3], wh[n][1], wl[n][1]);
-      }
-      uint8_t* p = a.w_ws + hs * (2LL * a.V / 64 * kTileBytes) + vt * kTileBytes;
-#pragma unroll
-      for (int part = 0; part < 2; ++part) {
-        __syncwarp();
-        stage_strip(part == 0 ? wh : wl, sg + St::kV, col0, lane);
-        __syncwarp();
-        uint8_t* dst = p + part * (a.V / 64) * kTileBytes;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t off = tile_off(i * 16 + (lane >> 1), (col0 >> 3) + (lane & 1));
-          *reinterpret_cast<uint4*>(dst + off) =
-              *reinterpret_cast<const uint4*>(smem + (c & 1) * St::kBytes + St::kV + off);
-        }
-      }
-    }
-    // Y = beta W
-#pragma unroll
-    for (int n = 0; n < 8; ++n) {
-      const float2 be = *reinterpret_cast<const float2*>(scal + n * 8 + 2 * (lane & 3));
-      x[n][0] *= be.x;
-      x[n][1] *= be.y;
-      x[n][2] *= be.x;
-      x[n][3] *= be.y;
-    }
-    if constexpr (kOut) {
-#pragma unroll
-      for (int kb = 0; kb < 4; ++kb) split_frag(x[2 * kb], x[2 * kb + 1], hi[kb], lo[kb]);
-      mul_lower_t(o, hi, lo, sg + St::kN + 2 * kTileBytes, sg + St::kN + 3 * kTileBytes, lane);
-      uint32_t ob[8][2];
-#pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        ob[n][0] = pack_bf16x2(a.scale * o[n][0], a.scale * o[n][1]);
-        ob[n][1] = pack_bf16x2(a.scale * o[n][2], a.scale * o[n][3]);
-      }
-      __syncwarp();
-      stage_strip(ob, sg + St::kV, col0, lane);
-      __syncwarp();
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = i * 16 + (lane >> 1);
-        if (row < live)
-          *reinterpret_cast<uint4*>(a.o + (t0 + row) * a.ldo + static_cast<long long>(h) * a.V + v0 +
-                                    (lane & 1) * 8) =
-              *reinterpret_cast<const uint4*>(smem + (c & 1) * St::kBytes + St::kV +
-                                              tile_off(row, (col0 >> 3) + (lane & 1)));
-      }
-    }
     // S' = e^{G_C} S + K^T (lambda Y)
-    split_scaled(x, scal + 128, 1.f, hi, lo, lane);
     const float whole = scal[192];
 #pragma unroll
-    for (int n = 0; n < KD / 8; ++n)
+    for (int n = 0; n < KD / 32; ++n)
 #pragma unroll
       for (int e = 0; e < 4; ++e) st[n][e] *= whole;
-    rank_update<KD>(st, hi, lo, sg + St::kK, lane);
-    __syncthreads();  // the stage may be filled again
+    named_barrier_sync(bars + kBarState, kGroupThreads);
+    rank_update<KD, false>(st, ex + Ex::kY, sg + St::kK, me);
+    if constexpr (kSave) {
+      // W as the three parts' tiles, turned through the own tokens of v
+      uint32_t f[3][4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        uint32_t p[3];
+        split3(x[i][0], x[i][1], p);
+#pragma unroll
+        for (int q = 0; q < 3; ++q) f[q][2 * i] = p[q];
+        split3(x[i][2], x[i][3], p);
+#pragma unroll
+        for (int q = 0; q < 3; ++q) f[q][2 * i + 1] = p[q];
+      }
+      uint8_t* p = a.w_ws + hs * (3LL * (a.V / 64) * kTileBytes) + (v0 / 64) * kTileBytes +
+                   tile_off(me.row(), ((v0 & 63) >> 3) + (lane & 1));
+#pragma unroll
+      for (int q = 0; q < 3; ++q)
+        *reinterpret_cast<uint4*>(p + q * (a.V / 64) * kTileBytes) =
+            turn_strip(f[q], sg + St::kV, stage + St::kV, group * 2, me);
+    }
   }
   if (kOut && a.state_out != nullptr)
-    store_state<KD>(st, a.state_out + head_state, a.V, v0, lane);
+    store_state<KD>(st, a.state_out + head_state, a.V, v0, me);
 }
 
-// Sums r[n][e] over the 16 rows of the strip (rows lane/4 and lane/4 + 8 of every column) and
-// leaves column n * 8 + 2 (lane % 4) + e's sum in lanes 0..3.
-__device__ __forceinline__ void strip_sums(float r[8][2], float* out, int lane) {
+// Sums r[i][e] over the 16 rows of the strip and leaves the sums of own tokens in `out`.
+__device__ __forceinline__ void strip_sums(float r[2][2], float* out, const ScanLane& me) {
 #pragma unroll
-  for (int n = 0; n < 8; ++n) {
+  for (int i = 0; i < 2; ++i) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
 #pragma unroll
-      for (int off = 4; off < 32; off <<= 1) r[n][e] += __shfl_xor_sync(0xffffffffu, r[n][e], off);
+      for (int off = 4; off < 32; off <<= 1) r[i][e] += __shfl_xor_sync(0xffffffffu, r[i][e], off);
     }
-    if (lane < 4) *reinterpret_cast<float2*>(out + n * 8 + 2 * lane) = make_float2(r[n][0], r[n][1]);
+    if (me.lane < 4) *reinterpret_cast<float2*>(out + me.token(i)) = make_float2(r[i][0], r[i][1]);
   }
 }
 
-// Backward, from the last chunk to the first.  D^T (16 x K per warp) is the gradient of the
-// state after the chunk:
+// Backward, from the last chunk to the first.  D^T is the gradient of the state after the
+// chunk:
 //   dY = scale P^T dO + lambda K D    U = dY - N^T (beta dY)    dX = dV = beta U
 //   dbeta = W . U    b = lambda beta (K D) . W  (for dg)
 //   D' = e^{G_C} D + Q^T (scale gamma dO) - K^T (gamma dX)
 // It writes dv, what dX has below BF16, D of every chunk and each strip's share of the two
 // row sums.
 template <int KD>
-__global__ void __launch_bounds__(kScanThreads, 1) delta_scan_bwd_kernel(const __grid_constant__ DeltaArgs a) {
-  using St = ScanStage<KD, true>;
+__global__ void __launch_bounds__(kStripThreads, 1)
+    delta_scan_bwd_kernel(const __grid_constant__ DeltaArgs a) {
+  using St = ScanStage<KD, 1, true>;
+  using Ex = ScanExchange<KD, true>;
   extern __shared__ __align__(128) uint8_t smem[];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int vt = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+  const bool side = threadIdx.x >= kGroupThreads;
+  const ScanLane me((threadIdx.x >> 5) & 3, threadIdx.x & 31);
+  const int lane = me.lane;
+  const int h = blockIdx.y, b = blockIdx.z;
   const int hk = h / (a.Hv / a.Hk);
-  const int col0 = warp * 16, v0 = vt * 64 + col0, strip = v0 / 16;
+  const int v0 = blockIdx.x * 16, strip = blockIdx.x;
   grid_dependency_wait();
   allow_dependent_launch();
   const long long start = seq_start(a.seq, b), end = seq_end(a.seq, b);
   const long long base = seq_base(a.seq, b);
   const int chunks = static_cast<int>((end - start + kChunk - 1) / kChunk);
   const uint32_t sbase = smem_u32(smem);
+  const uint32_t ex = sbase + 2 * St::kBytes;
+  float4* pbuf = reinterpret_cast<float4*>(smem + 2 * St::kBytes + Ex::kP) + me.warp * 64 + lane;
+  float4* rbuf =
+      reinterpret_cast<float4*>(smem + 2 * St::kBytes + Ex::kR) + me.warp * (KD / 32) * 32 + lane;
 
-  auto issue = [&](int c) {
-    const uint32_t st = sbase + (c & 1) * St::kBytes;
-    const long long t0 = start + static_cast<long long>(c) * kChunk;
-    const int live = static_cast<int>(end - t0 < kChunk ? end - t0 : kChunk);
-    load_rows<kScanThreads>(st + St::kQ, a.q + t0 * a.ldq + static_cast<long long>(hk) * KD, a.ldq,
-                            KD, live);
-    load_rows<kScanThreads>(st + St::kK, a.k + t0 * a.ldk + static_cast<long long>(hk) * KD, a.ldk,
-                            KD, live);
-    const long long hs = (base + c) * a.Hv + h;
-    const uint8_t* prep = a.prep + hs * kPrepBytes;
-    load_flat<kScanThreads>(st + St::kN, prep, 4 * kTileBytes);
-    load_flat<kScanThreads>(st + St::kScal, prep + kPrepTiles, 784);
-    load_rows<kScanThreads>(st + St::kV,
-                            a.dout + t0 * a.lddo + static_cast<long long>(h) * a.V + vt * 64, a.lddo,
-                            64, live);
-    const uint8_t* w = a.w_ws + hs * (2LL * a.V / 64 * kTileBytes) + vt * kTileBytes;
-    load_flat<kScanThreads>(st + St::kW, w, kTileBytes);
-    load_flat<kScanThreads>(st + St::kW + kTileBytes, w + (a.V / 64) * kTileBytes, kTileBytes);
-    cp_commit();
-  };
+  if (side) {
+    const int tid = threadIdx.x - kGroupThreads;
+    auto issue = [&](int c) {
+      const uint32_t st = sbase + (c & 1) * St::kBytes;
+      const long long t0 = start + static_cast<long long>(c) * kChunk;
+      const int live = static_cast<int>(end - t0 < kChunk ? end - t0 : kChunk);
+      const long long hs = (base + c) * a.Hv + h;
+      load_strips<kGroupThreads, 1>(
+          st + St::kV, a.dout + t0 * a.lddo + static_cast<long long>(h) * a.V + v0, a.lddo, live, tid);
+      const uint8_t* prep = a.prep + hs * kPrepBytes;
+      load_flat<kGroupThreads>(st + St::kTri, prep, 6 * kTriBytes, tid);
+      load_flat<kGroupThreads>(st + St::kScal, prep + kPrepTri, 784, tid);
+      load_rows<kGroupThreads>(st + St::kK, a.k + t0 * a.ldk + static_cast<long long>(hk) * KD, a.ldk,
+                               KD, live, tid);
+      const uint8_t* w = a.w_ws + hs * (3LL * (a.V / 64) * kTileBytes) + (v0 / 64) * kTileBytes;
+#pragma unroll
+      for (int p = 0; p < 3; ++p)
+        load_strips_tile<kGroupThreads, 1>(st + St::kW + p * strip_bytes<1>(),
+                                           w + p * (a.V / 64) * kTileBytes, (v0 & 63) >> 3, tid);
+      load_rows<kGroupThreads>(st + St::kQ, a.q + t0 * a.ldq + static_cast<long long>(hk) * KD, a.ldq,
+                               KD, live, tid);
+      cp_commit();
+    };
+    if (chunks > 0) issue(chunks - 1);
+    for (int c = chunks - 1; c >= 0; --c) {
+      cp_wait<0>();
+      __syncthreads();  // stage c has arrived, the other one is free, D can be read
+      const uint32_t sg = sbase + (c & 1) * St::kBytes;
+      const float* scal = reinterpret_cast<const float*>(smem + (c & 1) * St::kBytes + St::kScal);
+      // scale P^T dO
+      uint32_t dof[16];
+#pragma unroll
+      for (int kb = 0; kb < 4; ++kb)
+        ldsm4t(dof + 4 * kb,
+               sg + St::kV + strip_off((lane >> 3) & 1, kb * 16 + ((lane >> 4) << 3) + (lane & 7)));
+      float t[2][4];
+      zero_tiles(t);
+      tri_product<true, 1, 3, 3>(t, dof, 0, sg + St::kTri + 3 * kTriBytes, me);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        pbuf[i * 32] = make_float4(a.scale * t[i][0], a.scale * t[i][1], a.scale * t[i][2],
+                                   a.scale * t[i][3]);
+      bar_arrive(kBarA, kStripThreads);
+      if (c > 0) issue(c - 1);
+      // Q^T (scale gamma dO)
+      get_strip(t, sg + St::kV, 0, me);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float2 gm = *reinterpret_cast<const float2*>(scal + 64 + me.token(i));
+        const float sx = a.scale * gm.x, sy = a.scale * gm.y;
+        const float z[4] = {sx * t[i][0], sy * t[i][1], sx * t[i][2], sy * t[i][3]};
+        put_tile<3>(ex + Ex::kO, me.tile(i), lane, z);
+      }
+      named_barrier_sync(kBarSide, kGroupThreads);
+      float r[KD / 32][4];
+#pragma unroll
+      for (int n = 0; n < KD / 32; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) r[n][e] = 0.f;
+      rank_update<KD, false>(r, ex + Ex::kO, sg + St::kQ, me);
+#pragma unroll
+      for (int n = 0; n < KD / 32; ++n) rbuf[n * 32] = make_float4(r[n][0], r[n][1], r[n][2], r[n][3]);
+      bar_arrive(kBarB, kStripThreads);
+    }
+    return;
+  }
 
-  float d[KD / 8][4];
+  float d[KD / 32][4];
   const long long head_state = (static_cast<long long>(b) * a.Hv + h) * KD * a.V;
   if (a.dstate_out != nullptr) {
-    load_state<KD>(d, a.dstate_out + head_state, a.V, v0, lane);
+    load_state<KD>(d, a.dstate_out + head_state, a.V, v0, me);
   } else {
 #pragma unroll
-    for (int n = 0; n < KD / 8; ++n)
+    for (int n = 0; n < KD / 32; ++n)
 #pragma unroll
       for (int e = 0; e < 4; ++e) d[n][e] = 0.f;
   }
-  if (chunks > 0) issue(chunks - 1);
   for (int c = chunks - 1; c >= 0; --c) {
-    if (c > 0) {
-      issue(c - 1);
-      cp_wait<1>();
-    } else {
-      cp_wait<0>();
-    }
+    put_state<KD>(ex + Ex::kS, me.warp, lane, d);
     __syncthreads();
     uint8_t* stage = smem + (c & 1) * St::kBytes;
     const uint32_t sg = sbase + (c & 1) * St::kBytes;
@@ -435,140 +655,107 @@ __global__ void __launch_bounds__(kScanThreads, 1) delta_scan_bwd_kernel(const _
     const long long t0 = start + static_cast<long long>(c) * kChunk;
     const int live = static_cast<int>(end - t0 < kChunk ? end - t0 : kChunk);
     const long long hs = (base + c) * a.Hv + h;
+    // lambda K D
+    float y[2][4], w[2][4], t[2][4];
+    state_product<KD, 3>(y, ex + Ex::kS, sg + St::kK, me);
+    get_strip(w, sg + St::kW + 2 * strip_bytes<1>(), 0, me);
+#pragma unroll
+    for (int p = 1; p >= 0; --p) {
+      get_strip(t, sg + St::kW + p * strip_bytes<1>(), 0, me);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[i][e] += t[i][e];
+    }
+    float2 be[2];
+    float r[2][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float2 lm = *reinterpret_cast<const float2*>(scal + 128 + me.token(i));
+      be[i] = *reinterpret_cast<const float2*>(scal + me.token(i));
+      y[i][0] *= lm.x;
+      y[i][1] *= lm.y;
+      y[i][2] *= lm.x;
+      y[i][3] *= lm.y;
+      r[i][0] = be[i].x * fmaf(y[i][0], w[i][0], y[i][2] * w[i][2]);
+      r[i][1] = be[i].y * fmaf(y[i][1], w[i][1], y[i][3] * w[i][3]);
+    }
+    named_barrier_sync(kBarA, kStripThreads);  // scale P^T dO can be read
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float4 p = pbuf[i * 32];
+      y[i][0] += p.x;
+      y[i][1] += p.y;
+      y[i][2] += p.z;
+      y[i][3] += p.w;
+      const float u[4] = {-be[i].x * y[i][0], -be[i].y * y[i][1], -be[i].x * y[i][2],
+                          -be[i].y * y[i][3]};
+      put_tile<3>(ex + Ex::kX, me.tile(i), lane, u);
+    }
+    named_barrier_sync(kBarState, kGroupThreads);
+    // U = dY - N^T (beta dY)
+    tri_product<true, 3, 3, 3>(y, nullptr, ex + Ex::kX, sg + St::kTri, me);
+    float r2[2][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      r2[i][0] = fmaf(y[i][0], w[i][0], y[i][2] * w[i][2]);
+      r2[i][1] = fmaf(y[i][1], w[i][1], y[i][3] * w[i][3]);
+      // dX = beta U
+      const float2 gm = *reinterpret_cast<const float2*>(scal + 64 + me.token(i));
+      y[i][0] *= be[i].x;
+      y[i][1] *= be[i].y;
+      y[i][2] *= be[i].x;
+      y[i][3] *= be[i].y;
+      const float u[4] = {gm.x * y[i][0], gm.y * y[i][1], gm.x * y[i][2], gm.y * y[i][3]};
+      put_tile<3>(ex + Ex::kY, me.tile(i), lane, u);
+    }
     {
       uint8_t* p = a.d_ws + hs * KD * a.V * 4;
 #pragma unroll
-      for (int n = 0; n < KD / 8; ++n)
-        *reinterpret_cast<float4*>(p + frag_off(KD, strip, n, lane)) =
+      for (int n = 0; n < KD / 32; ++n)
+        *reinterpret_cast<float4*>(p + frag_off(KD, strip, me.warp * (KD / 32) + n, lane)) =
             make_float4(d[n][0], d[n][1], d[n][2], d[n][3]);
-    }
-    // D^T K^T, scaled by lambda
-    float y[8][4];
-#pragma unroll
-    for (int n = 0; n < 8; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) y[n][e] = 0.f;
-#pragma unroll
-    for (int kb = 0; kb < KD / 16; ++kb) {
-      uint32_t hi[4], lo[4];
-      split_frag(d[2 * kb], d[2 * kb + 1], hi, lo);
-      mul_rows_exact(y, hi, lo, sg + St::kK + (kb >> 2) * kTileBytes, (kb & 3) * 16, lane);
-    }
-    float w[8][4];
-    {
-      uint32_t wh[8][2], wl[8][2];
-      load_strip(wh, sg + St::kW, col0, lane);
-      load_strip(wl, sg + St::kW + kTileBytes, col0, lane);
-#pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        w[n][0] = bf_lo(wh[n][0]) + bf_lo(wl[n][0]);
-        w[n][1] = bf_hi(wh[n][0]) + bf_hi(wl[n][0]);
-        w[n][2] = bf_lo(wh[n][1]) + bf_lo(wl[n][1]);
-        w[n][3] = bf_hi(wh[n][1]) + bf_hi(wl[n][1]);
-      }
-    }
-    float* dots = a.dots + (hs * (a.V / 16) + strip) * 128;
-    {
-      float r[8][2];
-#pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        const int t = n * 8 + 2 * (lane & 3);
-        const float2 lm = *reinterpret_cast<const float2*>(scal + 128 + t);
-        const float2 be = *reinterpret_cast<const float2*>(scal + t);
-        y[n][0] *= lm.x;
-        y[n][1] *= lm.y;
-        y[n][2] *= lm.x;
-        y[n][3] *= lm.y;
-        r[n][0] = be.x * fmaf(y[n][0], w[n][0], y[n][2] * w[n][2]);
-        r[n][1] = be.y * fmaf(y[n][1], w[n][1], y[n][3] * w[n][3]);
-      }
-      strip_sums(r, dots, lane);
-    }
-    // + scale P^T dO
-    uint32_t dof[8][2];
-    load_strip(dof, sg + St::kV, col0, lane);
-    uint32_t hi[4][4], lo[4][4];
-    {
-      float p[8][4];
-#pragma unroll
-      for (int n = 0; n < 8; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) p[n][e] = 0.f;
-#pragma unroll
-      for (int kb = 0; kb < 4; ++kb) {
-        hi[kb][0] = dof[2 * kb][0];
-        hi[kb][1] = dof[2 * kb][1];
-        hi[kb][2] = dof[2 * kb + 1][0];
-        hi[kb][3] = dof[2 * kb + 1][1];
-      }
-      mul_lower<true>(p, hi, hi, sg + St::kN + 2 * kTileBytes, sg + St::kN + 3 * kTileBytes, lane);
-#pragma unroll
-      for (int n = 0; n < 8; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) y[n][e] = fmaf(a.scale, p[n][e], y[n][e]);
-    }
-    // U = dY - N^T (beta dY)
-    split_scaled(y, scal, -1.f, hi, lo, lane);
-    mul_lower<false>(y, hi, lo, sg + St::kN, sg + St::kN + kTileBytes, lane);
-    {
-      float r[8][2];
-#pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        r[n][0] = fmaf(y[n][0], w[n][0], y[n][2] * w[n][2]);
-        r[n][1] = fmaf(y[n][1], w[n][1], y[n][3] * w[n][3]);
-      }
-      strip_sums(r, dots + 64, lane);
-    }
-    // dX = beta U: dv, and what is left below BF16
-    uint32_t xh[8][2], xl[8][2];
-#pragma unroll
-    for (int n = 0; n < 8; ++n) {
-      const float2 be = *reinterpret_cast<const float2*>(scal + n * 8 + 2 * (lane & 3));
-      y[n][0] *= be.x;
-      y[n][1] *= be.y;
-      y[n][2] *= be.x;
-      y[n][3] *= be.y;
-      split2(y[n][0], y[n][1], xh[n][0], xl[n][0]);
-      split2(y[n][2], y[n][3], xh[n][1], xl[n][1]);
-    }
-    __syncwarp();
-    stage_strip(xh, sg + St::kW, col0, lane);
-    stage_strip(xl, sg + St::kW + kTileBytes, col0, lane);
-    __syncwarp();
-    {
-      uint8_t* xlo = a.x_ws + hs * (a.V / 64 * kTileBytes) + vt * kTileBytes;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = i * 16 + (lane >> 1);
-        const uint32_t off = tile_off(row, (col0 >> 3) + (lane & 1));
-        *reinterpret_cast<uint4*>(xlo + off) =
-            *reinterpret_cast<const uint4*>(stage + St::kW + kTileBytes + off);
-        if (row < live)
-          *reinterpret_cast<uint4*>(a.dv + (t0 + row) * a.lddv + static_cast<long long>(h) * a.V +
-                                    v0 + (lane & 1) * 8) =
-              *reinterpret_cast<const uint4*>(stage + St::kW + off);
-      }
     }
     // D' = e^{G_C} D + Q^T (scale gamma dO) - K^T (gamma dX)
     const float whole = scal[192];
 #pragma unroll
-    for (int n = 0; n < KD / 8; ++n)
+    for (int n = 0; n < KD / 32; ++n)
 #pragma unroll
       for (int e = 0; e < 4; ++e) d[n][e] *= whole;
-    split_scaled(y, scal + 64, -1.f, hi, lo, lane);
-    rank_update<KD>(d, hi, lo, sg + St::kK, lane);
+    named_barrier_sync(kBarState, kGroupThreads);
+    rank_update<KD, true>(d, ex + Ex::kY, sg + St::kK, me);
+    named_barrier_sync(kBarB, kStripThreads);  // the term of dO can be read
 #pragma unroll
-    for (int n = 0; n < 8; ++n) {
-      y[n][0] = bf_lo(dof[n][0]);
-      y[n][1] = bf_hi(dof[n][0]);
-      y[n][2] = bf_lo(dof[n][1]);
-      y[n][3] = bf_hi(dof[n][1]);
+    for (int n = 0; n < KD / 32; ++n) {
+      const float4 q = rbuf[n * 32];
+      d[n][0] += q.x;
+      d[n][1] += q.y;
+      d[n][2] += q.z;
+      d[n][3] += q.w;
     }
-    split_scaled(y, scal + 64, a.scale, hi, lo, lane);
-    rank_update<KD>(d, hi, lo, sg + St::kQ, lane);
-    __syncthreads();
+    // what leaves: dv, what dX has below BF16, the row sums (W's matrices of the own tokens
+    // are this warp's alone)
+    {
+      uint32_t xh[4], xl[4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        split2(y[i][0], y[i][1], xh[2 * i], xl[2 * i]);
+        split2(y[i][2], y[i][3], xh[2 * i + 1], xl[2 * i + 1]);
+      }
+      const int row = me.row();
+      const uint4 vh = turn_strip(xh, sg + St::kW, stage + St::kW, 0, me);
+      const uint4 vl = turn_strip(xl, sg + St::kW, stage + St::kW, 0, me);
+      *reinterpret_cast<uint4*>(a.x_ws + hs * (a.V / 64 * kTileBytes) + (v0 / 64) * kTileBytes +
+                                tile_off(row, ((v0 & 63) >> 3) + (lane & 1))) = vl;
+      if (row < live)
+        *reinterpret_cast<uint4*>(a.dv + (t0 + row) * a.lddv + static_cast<long long>(h) * a.V + v0 +
+                                  (lane & 1) * 8) = vh;
+      float* dots = a.dots + (hs * (a.V / 16) + strip) * 128;
+      strip_sums(r, dots, me);
+      strip_sums(r2, dots + 64, me);
+    }
   }
-  if (a.dstate_in != nullptr) store_state<KD>(d, a.dstate_in + head_state, a.V, v0, lane);
+  if (a.dstate_in != nullptr) store_state<KD>(d, a.dstate_in + head_state, a.V, v0, me);
 }
 
 }  // namespace gnorm

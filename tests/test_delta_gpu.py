@@ -147,8 +147,12 @@ def call(x, **kw):
     return dict(zip(("o", "S") + GRADS, (o, S) + grads))
 
 
-def check(x):
+def check(x, by_head=False):
     got, ref = call(x), recurrence(x)
+    if by_head:
+        ref["size"]["dv"] = ref["dv"].square().mean((0, 2), keepdim=True).sqrt()
+        for n in ("dbeta", "dg"):
+            ref["size"][n] = ref["size"][n].amax(0, keepdim=True)
     n = sum(x["lens"])
     for name, t in got.items():
         if t is None:
@@ -222,6 +226,18 @@ def test_beta_zero_and_one():
     x["beta"][:40] = 0.0
     x["beta"][40:100] = 1.0
     check(x)
+
+
+def test_repeated_keys():
+    """The same key at every token: the triangular system at its least well conditioned.  dv is
+    its solution, dv_t = beta_t sum_i T_ti dY_i over the chunk's tokens: where every key is the
+    same, dY_i and dY_(i+1) differ by one row of do and T takes the differences, so a row's
+    terms are as large as the head's rows, however small the row itself: they are compared with
+    the head's RMS, and dbeta and dg, products with these rows, with the head's largest."""
+    x = make([192], 1, 1, 128, 128, decay=0.01)
+    x["k"] = x["k"][:1].expand(192, 1, 128).contiguous()
+    x["beta"][:] = 0.9
+    check(x, by_head=True)
 
 
 def test_what_lies_behind_the_last_sequence():
