@@ -11,53 +11,55 @@ import ctypes
 import torch
 
 from ._lib import GnormBlockBwdDesc, GnormBlockFwdDesc, lib
-from .gnorm import _check, _device_buffer, _ptr, _same, _stream, _vec
+from .gnorm import _check, _device_buffer, _on, _ptr, _same, _stream, _vec
 
 __all__ = ["gnorm_block_fwd", "gnorm_block_bwd", "gnorm_block_bwd_workspace_bytes",
            "block_rmsnorm", "BlockRMSNormFunction", "BlockRMSNorm"]
 
 _RES = (torch.bfloat16, torch.float32)
+_BF16 = (torch.bfloat16,)
+_FP32 = (torch.float32,)
 
 
-def _rows(t: torch.Tensor, name: str, dtypes):
-    """(M, N, row stride): contiguous of any rank, or a 2-D view with unit column stride."""
+def _rows(t: torch.Tensor, name: str, dtypes, like=None):
+    """Row stride of rows of the last dimension: contiguous of any rank, or a 2-D view with unit
+    column stride."""
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be one of {dtypes}, got {t.dtype}")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() < 1:
+    if like is not None:
+        if t.shape != like.shape or t.device != like.device:
+            _same(like, t, "a", name)
+    elif t.dim() < 1:
         raise ValueError(f"{name} must have a last dimension N")
-    N = t.shape[-1]
     if t.is_contiguous():
-        return (t.numel() // N if N else 0), N, N
+        return t.shape[-1]
     if t.dim() == 2 and t.stride(1) == 1:
-        return t.shape[0], N, (t.stride(0) if t.shape[0] > 1 else N)
+        return t.stride(0) if t.shape[0] > 1 else t.shape[1]
     raise ValueError(f"{name}: rows need unit column stride (2-D row-strided views or "
                      "contiguous tensors)")
 
 
-def _common(a, r, g, w1, w2, alpha):
-    M, N, lda = _rows(a, "a", (torch.bfloat16,))
-    _same(a, r, "a", "r")
-    _, _, ldr = _rows(r, "r", _RES)
-    ldg = 0
+def _common(d, a, r, g, w1, w2, alpha):
+    """Checks the inputs that both calls share and puts them into the descriptor."""
+    d.lda = _rows(a, "a", _BF16)
+    N = a.shape[-1]
+    M = a.numel() // N if N else 0
+    d.ldr = _rows(r, "r", _RES, a)
     if g is not None:
-        _same(a, g, "a", "g")
-        _, _, ldg = _rows(g, "g", (torch.bfloat16,))
-    _vec(w1, N, _RES, "w1", a.device)
-    _vec(w2, N, (w1.dtype,), "w2", a.device)
+        d.ldg = _rows(g, "g", _BF16, a)
+        d.g = _ptr(g)
+    dev = a.device
+    _vec(w1, N, _RES, "w1", dev)
+    _vec(w2, N, (w1.dtype,), "w2", dev)
     if alpha is not None:
-        _vec(alpha, 1, (torch.float32,), "alpha", a.device)
-    return M, N, dict(a=_ptr(a), lda=lda, r=_ptr(r), ldr=ldr, g=_ptr(g), ldg=ldg, w1=_ptr(w1),
-                      w2=_ptr(w2), w_fp32=int(w1.dtype == torch.float32),
-                      res_fp32=int(r.dtype == torch.float32), alpha=_ptr(alpha), M=M, N=N)
-
-
-def _out(t, like, dtype, name):
-    if t is None:
-        return torch.empty(like.shape, dtype=dtype, device=like.device)
-    _same(like, t, "a", name)
-    return t
+        _vec(alpha, 1, _FP32, "alpha", dev)
+        d.alpha = alpha.data_ptr()
+    d.a, d.r, d.w1, d.w2 = _ptr(a), _ptr(r), _ptr(w1), _ptr(w2)
+    d.w_fp32, d.res_fp32 = w1.dtype == torch.float32, r.dtype == torch.float32
+    d.M, d.N = M, N
+    return M, N, dev
 
 
 def gnorm_block_fwd(a, r, w1, w2, eps: float = 1e-6, *, g=None, alpha=None, eps2=None, h=None,
@@ -67,21 +69,26 @@ def gnorm_block_fwd(a, r, w1, w2, eps: float = 1e-6, *, g=None, alpha=None, eps2
     h = r + alpha * silu(g) * rmsnorm(a) * w1 and z = rmsnorm(h) * w2.  a, g: BF16 rows; r:
     BF16 or FP32 rows (h has its type); w1, w2: both BF16 or both FP32 [N]; alpha: FP32 [1] on
     the device, None = 1; g None = no gate; eps2: the second norm's eps (None = eps)."""
-    M, N, c = _common(a, r, g, w1, w2, alpha)
-    h = _out(h, a, r.dtype, "h")
-    z = _out(z, a, torch.bfloat16, "z")
-    _, _, ldh = _rows(h, "h", (r.dtype,))
-    _, _, ldz = _rows(z, "z", (torch.bfloat16,))
-    if rstd1 is None or rstd2 is None:
-        both = torch.empty((2, M), dtype=torch.float32, device=a.device)
-        rstd1 = both[0] if rstd1 is None else rstd1
-        rstd2 = both[1] if rstd2 is None else rstd2
-    for t, n in ((rstd1, "rstd1"), (rstd2, "rstd2")):
-        _vec(t, M, (torch.float32,), n, a.device)
-    d = GnormBlockFwdDesc(eps1=float(eps), eps2=float(eps if eps2 is None else eps2), h=_ptr(h),
-                          ldh=ldh, z=_ptr(z), ldz=ldz, rstd1=_ptr(rstd1), rstd2=_ptr(rstd2), **c)
-    with torch.cuda.device(a.device):
-        st = lib.gnorm_block_fwd(ctypes.byref(d), _stream(stream, a.device))
+    d = GnormBlockFwdDesc()
+    M, _, dev = _common(d, a, r, g, w1, w2, alpha)
+    if h is None:
+        h = torch.empty(a.shape, dtype=r.dtype, device=dev)
+    if z is None:
+        z = torch.empty(a.shape, dtype=torch.bfloat16, device=dev)
+    if rstd1 is None and rstd2 is None:
+        rstd1, rstd2 = torch.empty((2, M), dtype=torch.float32, device=dev).unbind()
+    else:
+        if rstd1 is None:
+            rstd1 = torch.empty(M, dtype=torch.float32, device=dev)
+        if rstd2 is None:
+            rstd2 = torch.empty(M, dtype=torch.float32, device=dev)
+        _vec(rstd1, M, _FP32, "rstd1", dev)
+        _vec(rstd2, M, _FP32, "rstd2", dev)
+    d.eps1, d.eps2 = eps, eps if eps2 is None else eps2
+    d.h, d.ldh, d.z, d.ldz = _ptr(h), _rows(h, "h", (r.dtype,), a), _ptr(z), _rows(z, "z", _BF16, a)
+    d.rstd1, d.rstd2 = _ptr(rstd1), _ptr(rstd2)
+    with _on(dev):
+        st = lib.gnorm_block_fwd(ctypes.byref(d), _stream(stream, dev))
     _check(st, "gnorm_block_fwd")
     return h, z, rstd1, rstd2
 
@@ -98,51 +105,52 @@ def gnorm_block_bwd(dh, dz, a, r, w1, w2, rstd1, rstd2, *, g=None, alpha=None, d
 
     dh: gradient of h through the residual (r's type; None = zero); dz: BF16 gradient of z;
     rstd1, rstd2 as the forward wrote them.  dw1 and dw2 are FP32 if dw_fp32 else BF16."""
-    M, N, c = _common(a, r, g, w1, w2, alpha)
-    dev = a.device
-    lddh = 0
+    d = GnormBlockBwdDesc()
+    M, N, dev = _common(d, a, r, g, w1, w2, alpha)
     if dh is not None:
-        _same(a, dh, "a", "dh")
-        _, _, lddh = _rows(dh, "dh", (r.dtype,))
-    _same(a, dz, "a", "dz")
-    _, _, lddz = _rows(dz, "dz", (torch.bfloat16,))
-    for t, n in ((rstd1, "rstd1"), (rstd2, "rstd2")):
-        _vec(t, M, (torch.float32,), n, dev)
-    da = _out(da, a, torch.bfloat16, "da")
-    dr = _out(dr, a, r.dtype, "dr")
-    _, _, ldda = _rows(da, "da", (torch.bfloat16,))
-    _, _, lddr = _rows(dr, "dr", (r.dtype,))
-    lddg = 0
+        d.dh, d.lddh = _ptr(dh), _rows(dh, "dh", (r.dtype,), a)
+    d.dz, d.lddz = _ptr(dz), _rows(dz, "dz", _BF16, a)
+    _vec(rstd1, M, _FP32, "rstd1", dev)
+    _vec(rstd2, M, _FP32, "rstd2", dev)
+    d.rstd1, d.rstd2 = _ptr(rstd1), _ptr(rstd2)
+    if da is None:
+        da = torch.empty(a.shape, dtype=torch.bfloat16, device=dev)
+    if dr is None:
+        dr = torch.empty(a.shape, dtype=r.dtype, device=dev)
+    d.da, d.ldda = _ptr(da), _rows(da, "da", _BF16, a)
+    d.dr, d.lddr = _ptr(dr), _rows(dr, "dr", (r.dtype,), a)
     if g is not None:
-        dg = _out(dg, a, torch.bfloat16, "dg")
-        _, _, lddg = _rows(dg, "dg", (torch.bfloat16,))
+        if dg is None:
+            dg = torch.empty(a.shape, dtype=torch.bfloat16, device=dev)
+        d.dg, d.lddg = _ptr(dg), _rows(dg, "dg", _BF16, a)
     elif dg is not None:
         raise ValueError("dg without a gate")
     wt = torch.float32 if dw_fp32 else torch.bfloat16
     dw1 = torch.empty(N, dtype=wt, device=dev) if dw1 is None else dw1
     dw2 = torch.empty(N, dtype=wt, device=dev) if dw2 is None else dw2
-    for t, n in ((dw1, "dw1"), (dw2, "dw2")):
-        _vec(t, N, (wt,), n, dev)
+    _vec(dw1, N, (wt,), "dw1", dev)
+    _vec(dw2, N, (wt,), "dw2", dev)
+    d.dw1, d.dw2, d.dw_fp32 = _ptr(dw1), _ptr(dw2), bool(dw_fp32)
     if alpha is not None:
         dalpha = torch.empty_like(alpha) if dalpha is None else dalpha
-        _vec(dalpha, 1, (torch.float32,), "dalpha", dev)
+        _vec(dalpha, 1, _FP32, "dalpha", dev)
+        d.dalpha = dalpha.data_ptr()
     elif dalpha is not None:
         raise ValueError("dalpha without an alpha")
-    with torch.cuda.device(dev):
+    with _on(dev):
         if workspace_buf is None:
             # from torch's allocator for every call: ordered on the stream that uses it, and
             # owned by the graph when the call is captured
-            with torch.cuda.stream(stream or torch.cuda.current_stream(dev)):
-                workspace_buf = torch.empty(gnorm_block_bwd_workspace_bytes(M, N),
-                                            dtype=torch.uint8, device=dev)
+            need = gnorm_block_bwd_workspace_bytes(M, N)
+            if stream is None:
+                workspace_buf = torch.empty(need, dtype=torch.uint8, device=dev)
+            else:
+                with torch.cuda.stream(stream):
+                    workspace_buf = torch.empty(need, dtype=torch.uint8, device=dev)
         else:
             _device_buffer(workspace_buf, "workspace_buf", dev)
-        d = GnormBlockBwdDesc(
-            dh=_ptr(dh), lddh=lddh, dz=_ptr(dz), lddz=lddz, rstd1=_ptr(rstd1), rstd2=_ptr(rstd2),
-            da=_ptr(da), ldda=ldda, dr=_ptr(dr), lddr=lddr, dg=_ptr(dg), lddg=lddg,
-            dw1=_ptr(dw1), dw2=_ptr(dw2), dw_fp32=int(bool(dw_fp32)), dalpha=_ptr(dalpha),
-            workspace=_ptr(workspace_buf),
-            workspace_bytes=workspace_buf.numel() * workspace_buf.element_size(), **c)
+        d.workspace = _ptr(workspace_buf)
+        d.workspace_bytes = workspace_buf.numel() * workspace_buf.element_size()
         st = lib.gnorm_block_bwd(ctypes.byref(d), _stream(stream, dev))
     _check(st, "gnorm_block_bwd")
     return da, dr, dg, dw1, dw2, dalpha

@@ -11,7 +11,7 @@ import torch
 
 from ._lib import GnormDeltaBwdDesc, GnormDeltaFwdDesc, GnormDeltaIn, GnormDeltaStepDesc, lib
 from .autograd import gated_rmsnorm
-from .gnorm import _check, _device_buffer, _ptr, _stream
+from .gnorm import _check, _device_buffer, _on, _ptr, _stream
 
 __all__ = ["gnorm_delta_fwd", "gnorm_delta_bwd", "gnorm_delta_step",
            "gnorm_delta_workspace_bytes", "GatedDeltaRuleFunction", "gated_delta_rule",
@@ -19,38 +19,34 @@ __all__ = ["gnorm_delta_fwd", "gnorm_delta_bwd", "gnorm_delta_step",
 
 _BF16 = (torch.bfloat16,)
 _FP32 = (torch.float32,)
+_BETA = _BF16 + _FP32
 
 
-def _tokens(t: torch.Tensor, name: str, tail, dtypes, lead=None, device=None):
-    """Token stride of a [T, *tail] or [B, L, *tail] CUDA tensor whose heads are packed within
-    a token (tokens may be any distance apart, e.g. a slice of a wider projection)."""
+def _tokens(t: torch.Tensor, name: str, tail, dtypes, lead, device):
+    """Token stride of a [*lead, *tail] CUDA tensor ([T, ...] or [B, L, ...]) whose heads are
+    packed within a token (tokens may be any distance apart, e.g. a slice of a wider
+    projection)."""
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be one of {dtypes}, got {t.dtype}")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if device is not None and t.device != device:
+    if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
-    n = len(tail)
-    if t.dim() - n not in (1, 2) or tuple(t.shape[-n:]) != tuple(tail):
-        raise ValueError(f"{name} must be [T, {', '.join(map(str, tail))}] (or [B, L, ...]), got "
-                         f"{tuple(t.shape)}")
-    if lead is not None and tuple(t.shape[:-n]) != tuple(lead):
-        raise ValueError(f"{name} {tuple(t.shape)} has other tokens than {tuple(lead)}")
-    width = 1
-    for d in tail:
-        width *= d
+    if t.shape != lead + tail:
+        raise ValueError(f"{name} must be {lead + tail}, got {tuple(t.shape)}")
+    width = tail[0] * tail[1] if len(tail) == 2 else tail[0]
     if t.is_contiguous() or t.numel() == 0:
         return width
-    st = t.stride()
+    st, n = t.stride(), len(lead)
     want = 1
-    for i in range(n):
-        if t.shape[-1 - i] > 1 and st[-1 - i] != want:
+    for size, step in zip(tail[::-1], st[:n - 1:-1]):
+        if size > 1 and step != want:
             raise ValueError(f"{name}: the heads of a token must be packed, strides {st}")
-        want *= t.shape[-1 - i]
-    if t.dim() - n == 1:
-        return st[0] if t.shape[0] > 1 else width
-    ld = st[1] if t.shape[1] > 1 else (st[0] if t.shape[0] > 1 else width)
-    if t.shape[0] > 1 and st[0] != ld * t.shape[1]:
+        want *= size
+    if n == 1:
+        return st[0] if lead[0] > 1 else width
+    ld = st[1] if lead[1] > 1 else (st[0] if lead[0] > 1 else width)
+    if lead[0] > 1 and st[0] != ld * lead[1]:
         raise ValueError(f"{name}: tokens must be evenly spaced over the batch, strides {st}")
     return ld
 
@@ -60,25 +56,27 @@ def _state(t, name: str, shape, device):
         return
     if t.dtype != torch.float32:
         raise TypeError(f"{name} must be float32, got {t.dtype}")
-    if t.device != device or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+    if t.device != device or not t.is_contiguous() or t.shape != shape:
         raise ValueError(f"{name} must be a contiguous {tuple(shape)} tensor on {device}, got "
                          f"{tuple(t.shape)} on {t.device}")
 
 
-def _inputs(q, k, v, g, beta, scale, cu_seqlens, initial_state):
-    """(descriptor, leading shape, state shape) of the inputs that all calls share."""
+def _inputs(d, q, k, v, g, beta, scale, cu_seqlens, initial_state):
+    """Checks the inputs that both calls share and puts them into the descriptor; returns the
+    leading and the state shape."""
     if q.dim() not in (3, 4) or v.dim() != q.dim():
         raise ValueError("q, k and v must be [T, heads, dim] or [B, L, heads, dim]")
-    lead, (Hk, K), (Hv, V) = tuple(q.shape[:-2]), q.shape[-2:], v.shape[-2:]
+    lead, qk, vv = q.shape[:-2], q.shape[-2:], v.shape[-2:]
+    (Hk, K), (Hv, V) = qk, vv
     dev = q.device
-    d = GnormDeltaIn(ldq=_tokens(q, "q", (Hk, K), _BF16),
-                     ldk=_tokens(k, "k", (Hk, K), _BF16, lead, dev),
-                     ldv=_tokens(v, "v", (Hv, V), _BF16, lead, dev),
-                     ldg=_tokens(g, "g", (Hv,), _FP32, lead, dev),
-                     ldbeta=_tokens(beta, "beta", (Hv,), _BF16 + _FP32, lead, dev),
-                     q=_ptr(q), k=_ptr(k), v=_ptr(v), g=_ptr(g), beta=_ptr(beta),
-                     beta_fp32=int(beta.dtype == torch.float32), Hk=Hk, Hv=Hv, K=K, V=V,
-                     scale=float(K ** -0.5 if scale is None else scale))
+    d.ldq, d.q = _tokens(q, "q", qk, _BF16, lead, dev), _ptr(q)
+    d.ldk, d.k = _tokens(k, "k", qk, _BF16, lead, dev), _ptr(k)
+    d.ldv, d.v = _tokens(v, "v", vv, _BF16, lead, dev), _ptr(v)
+    d.ldg, d.g = _tokens(g, "g", (Hv,), _FP32, lead, dev), _ptr(g)
+    d.ldbeta, d.beta = _tokens(beta, "beta", (Hv,), _BETA, lead, dev), _ptr(beta)
+    d.beta_fp32 = beta.dtype == torch.float32
+    d.Hk, d.Hv, d.K, d.V = Hk, Hv, K, V
+    d.scale = K ** -0.5 if scale is None else scale
     if cu_seqlens is not None:
         if len(lead) != 1:
             raise ValueError("cu_seqlens goes with [T, heads, dim] tensors")
@@ -95,7 +93,7 @@ def _inputs(q, k, v, g, beta, scale, cu_seqlens, initial_state):
     shape = (d.B, Hv, K, V)
     _state(initial_state, "initial_state", shape, dev)
     d.initial_state = _ptr(initial_state)
-    return d, lead, shape
+    return lead, shape
 
 
 def gnorm_delta_workspace_bytes(T: int, B: int, Hv: int, K: int, V: int,
@@ -128,21 +126,22 @@ def gnorm_delta_fwd(q, k, v, g, beta, *, scale=None, cu_seqlens=None, initial_st
     packs B sequences into the T tokens; without it [T, ...] is one sequence and [B, L, ...]
     are B.  States are FP32 [B, Hv, K, V].  Rows of o behind the last sequence are zero if this
     call allocates o, and left as they are in an o that is passed in."""
-    d, lead, shape = _inputs(q, k, v, g, beta, scale, cu_seqlens, initial_state)
+    f = GnormDeltaFwdDesc()
+    d = getattr(f, "in")  # shares f's memory
+    lead, shape = _inputs(d, q, k, v, g, beta, scale, cu_seqlens, initial_state)
     dev = q.device
     own = o is None
     if own:
         o = torch.empty(v.shape, dtype=torch.bfloat16, device=dev)
-    ldo = _tokens(o, "o", v.shape[-2:], _BF16, lead, dev)
+    f.ldo, f.o = _tokens(o, "o", v.shape[-2:], _BF16, lead, dev), _ptr(o)
     if final_state is None and output_final_state:
         final_state = torch.empty(shape, dtype=torch.float32, device=dev)
     _state(final_state, "final_state", shape, dev)
-    with torch.cuda.device(dev):
+    f.final_state = _ptr(final_state)
+    f.zero_tail = own and cu_seqlens is not None
+    with _on(dev):
         ws = _workspace(workspace_buf, d, False, dev, stream)
-        f = GnormDeltaFwdDesc(o=_ptr(o), ldo=ldo, final_state=_ptr(final_state),
-                              zero_tail=int(own and cu_seqlens is not None), workspace=_ptr(ws),
-                              workspace_bytes=ws.numel() * ws.element_size())
-        setattr(f, "in", d)
+        f.workspace, f.workspace_bytes = _ptr(ws), ws.numel() * ws.element_size()
         st = lib.gnorm_delta_fwd(ctypes.byref(f), _stream(stream, dev))
     _check(st, "gnorm_delta_fwd")
     return o, final_state
@@ -157,32 +156,34 @@ def gnorm_delta_bwd(do, q, k, v, g, beta, *, scale=None, cu_seqlens=None, initia
     dq, dk and dv are BF16, dg is FP32, dbeta has beta's type; dinitial_state is None without
     an initial state.  Rows behind the last sequence are zero in gradients that this call
     allocates; if any is passed in, they are left as they are in all of them."""
-    d, lead, shape = _inputs(q, k, v, g, beta, scale, cu_seqlens, initial_state)
+    b = GnormDeltaBwdDesc()
+    d = getattr(b, "in")  # shares b's memory
+    lead, shape = _inputs(d, q, k, v, g, beta, scale, cu_seqlens, initial_state)
     dev = q.device
-    lddo = _tokens(do, "do", v.shape[-2:], _BF16, lead, dev)
+    qk, vv, gb = q.shape[-2:], v.shape[-2:], g.shape[-1:]
+    b.lddo, b.d_o = _tokens(do, "do", vv, _BF16, lead, dev), _ptr(do)
     _state(dfinal_state, "dfinal_state", shape, dev)
-    outs = [dq, dk, dv, dg, dbeta]
-    own = all(t is None for t in outs)
-    like = [q, k, v, g, beta]
-    outs = [torch.empty(x.shape, dtype=x.dtype, device=dev) if t is None else t
-            for t, x in zip(outs, like)]
-    if not own and cu_seqlens is not None and any(t is None for t in (dq, dk, dv, dg, dbeta)):
+    given = [t is not None for t in (dq, dk, dv, dg, dbeta)]
+    if cu_seqlens is not None and any(given) and not all(given):
         raise ValueError("with cu_seqlens pass all of dq, dk, dv, dg and dbeta, or none")
-    ld = [_tokens(t, n, x.shape[len(lead):], (x.dtype,), lead, dev)
-          for t, n, x in zip(outs, ("dq", "dk", "dv", "dg", "dbeta"), like)]
+    dq = torch.empty(q.shape, dtype=q.dtype, device=dev) if dq is None else dq
+    dk = torch.empty(k.shape, dtype=k.dtype, device=dev) if dk is None else dk
+    dv = torch.empty(v.shape, dtype=v.dtype, device=dev) if dv is None else dv
+    dg = torch.empty(g.shape, dtype=g.dtype, device=dev) if dg is None else dg
+    dbeta = torch.empty(beta.shape, dtype=beta.dtype, device=dev) if dbeta is None else dbeta
+    b.lddq, b.dq = _tokens(dq, "dq", qk, _BF16, lead, dev), _ptr(dq)
+    b.lddk, b.dk = _tokens(dk, "dk", qk, _BF16, lead, dev), _ptr(dk)
+    b.lddv, b.dv = _tokens(dv, "dv", vv, _BF16, lead, dev), _ptr(dv)
+    b.lddg, b.dg = _tokens(dg, "dg", gb, _FP32, lead, dev), _ptr(dg)
+    b.lddbeta, b.dbeta = _tokens(dbeta, "dbeta", gb, (beta.dtype,), lead, dev), _ptr(dbeta)
     if dinitial_state is None and initial_state is not None:
         dinitial_state = torch.empty(shape, dtype=torch.float32, device=dev)
     _state(dinitial_state, "dinitial_state", shape, dev)
-    dq, dk, dv, dg, dbeta = outs
-    with torch.cuda.device(dev):
+    b.dfinal_state, b.dinitial_state = _ptr(dfinal_state), _ptr(dinitial_state)
+    b.zero_tail = cu_seqlens is not None and not any(given)
+    with _on(dev):
         ws = _workspace(workspace_buf, d, True, dev, stream)
-        b = GnormDeltaBwdDesc(d_o=_ptr(do), lddo=lddo, dfinal_state=_ptr(dfinal_state),
-                              dq=_ptr(dq), lddq=ld[0], dk=_ptr(dk), lddk=ld[1], dv=_ptr(dv),
-                              lddv=ld[2], dg=_ptr(dg), lddg=ld[3], dbeta=_ptr(dbeta),
-                              lddbeta=ld[4], dinitial_state=_ptr(dinitial_state),
-                              zero_tail=int(own and cu_seqlens is not None), workspace=_ptr(ws),
-                              workspace_bytes=ws.numel() * ws.element_size())
-        setattr(b, "in", d)
+        b.workspace, b.workspace_bytes = _ptr(ws), ws.numel() * ws.element_size()
         st = lib.gnorm_delta_bwd(ctypes.byref(b), _stream(stream, dev))
     _check(st, "gnorm_delta_bwd")
     return dq, dk, dv, dg, dbeta, dinitial_state
@@ -198,32 +199,36 @@ def gnorm_delta_step(q, k, v, g, beta, state, *, slots=None, scale=None, o=None,
     order."""
     if q.dim() != 3 or v.dim() != 3:
         raise ValueError("q, k and v must be [B, heads, dim]")
-    lead, (Hk, K), (Hv, V) = tuple(q.shape[:1]), q.shape[1:], v.shape[1:]
+    lead, qk, vv = q.shape[:1], q.shape[1:], v.shape[1:]
+    (Hk, K), (Hv, V) = qk, vv
     dev = q.device
     if state.dtype != torch.float32:
         raise TypeError(f"state must be float32, got {state.dtype}")
-    if state.dim() != 4 or tuple(state.shape[1:]) != (Hv, K, V) or state.device != dev or \
-            (state.numel() and not state[0].is_contiguous()):
+    if state.dim() != 4 or state.shape[1:] != (Hv, K, V) or state.device != dev or \
+            not (state.is_contiguous() or state[:1].is_contiguous()):
         raise ValueError(f"state must be [pool, {Hv}, {K}, {V}] on {dev} with packed slots, got "
                          f"{tuple(state.shape)} on {state.device}")
     if slots is not None:
         if slots.dtype != torch.int32:
             raise TypeError(f"slots must be int32, got {slots.dtype}")
-        if tuple(slots.shape) != lead or not slots.is_contiguous() or slots.device != dev:
+        if slots.shape != lead or not slots.is_contiguous() or slots.device != dev:
             raise ValueError(f"slots must be a contiguous [{lead[0]}] tensor on {dev}")
     if o is None:
         o = torch.empty(v.shape, dtype=torch.bfloat16, device=dev)
-    d = GnormDeltaStepDesc(
-        q=_ptr(q), ldq=_tokens(q, "q", (Hk, K), _BF16),
-        k=_ptr(k), ldk=_tokens(k, "k", (Hk, K), _BF16, lead, dev),
-        v=_ptr(v), ldv=_tokens(v, "v", (Hv, V), _BF16, lead, dev),
-        g=_ptr(g), ldg=_tokens(g, "g", (Hv,), _FP32, lead, dev),
-        beta=_ptr(beta), ldbeta=_tokens(beta, "beta", (Hv,), _BF16 + _FP32, lead, dev),
-        beta_fp32=int(beta.dtype == torch.float32), B=lead[0], Hk=Hk, Hv=Hv, K=K, V=V,
-        scale=float(K ** -0.5 if scale is None else scale), state=_ptr(state),
-        ldstate=state.stride(0) if state.shape[0] > 1 else Hv * K * V, pool=state.shape[0],
-        slots=_ptr(slots), o=_ptr(o), ldo=_tokens(o, "o", (Hv, V), _BF16, lead, dev))
-    with torch.cuda.device(dev):
+    d = GnormDeltaStepDesc()
+    d.ldq, d.q = _tokens(q, "q", qk, _BF16, lead, dev), _ptr(q)
+    d.ldk, d.k = _tokens(k, "k", qk, _BF16, lead, dev), _ptr(k)
+    d.ldv, d.v = _tokens(v, "v", vv, _BF16, lead, dev), _ptr(v)
+    d.ldg, d.g = _tokens(g, "g", (Hv,), _FP32, lead, dev), _ptr(g)
+    d.ldbeta, d.beta = _tokens(beta, "beta", (Hv,), _BETA, lead, dev), _ptr(beta)
+    d.beta_fp32 = beta.dtype == torch.float32
+    d.B, d.Hk, d.Hv, d.K, d.V = lead[0], Hk, Hv, K, V
+    d.scale = K ** -0.5 if scale is None else scale
+    d.state, d.pool = _ptr(state), state.shape[0]
+    d.ldstate = state.stride(0) if state.shape[0] > 1 else Hv * K * V
+    d.slots = _ptr(slots)
+    d.ldo, d.o = _tokens(o, "o", vv, _BF16, lead, dev), _ptr(o)
+    with _on(dev):
         st = lib.gnorm_delta_step(ctypes.byref(d), _stream(stream, dev))
     _check(st, "gnorm_delta_step")
     return o

@@ -107,13 +107,33 @@ def gnorm_set_tuning(**knobs) -> None:
 # ----------------------------------------------------------------------------- helpers
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr() if t.numel() else 0)
+    return t.data_ptr() or None if t is not None and t.numel() else None
 
 
-def _stream(stream, device) -> ctypes.c_void_p:
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    return ctypes.c_void_p(stream.cuda_stream)
+def _stream(stream, device):
+    if stream is not None:
+        return stream.cuda_stream
+    if device.index is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+class _Here:
+    """What `with _on(device)` enters when the device is the current one already: nothing (a
+    guard's two driver calls are a good part of a small call)."""
+
+    def __enter__(self):
+        pass
+
+    def __exit__(self, *exc):
+        return False
+
+
+_here = _Here()
+
+
+def _on(device):
+    return _here if torch.cuda.current_device() == device.index else torch.cuda.device(device)
 
 
 def _mat(t: torch.Tensor, name: str):
@@ -268,7 +288,7 @@ def gnorm_fwd(x, g, w, eps: float = 1e-6, *, y=None, rstd=None, stream=None):
     x, g: BF16 rows (contiguous, or 2-D views with any row stride); w: BF16 or FP32 [N];
     rstd: FP32 [M].  y is allocated packed unless given (it may be a strided view)."""
     d, y, rstd = _fwd_desc(x, g, w, eps, y, rstd)
-    with torch.cuda.device(x.device):
+    with _on(x.device):
         st = lib.gnorm_fwd_ex(ctypes.byref(d), _stream(stream, x.device))
     _check(st, "gnorm_fwd")
     return y, rstd
@@ -282,7 +302,7 @@ def gnorm_bwd(dy, x, g, w, rstd, *, dx=None, dg=None, dw=None, dw_fp32: bool = F
                               workspace_buf)
     if rstd is None:
         raise ValueError("rstd is required")
-    with torch.cuda.device(x.device):
+    with _on(x.device):
         st = lib.gnorm_bwd_ex(ctypes.byref(d), _stream(stream, x.device))
     _check(st, "gnorm_bwd")
     return dx, dg, dw
@@ -295,7 +315,7 @@ def gnorm_ckpt_step(x, g, w, eps: float, dy, *, y=None, rstd=None, dx=None, dg=N
     fd, y, rstd = _fwd_desc(x, g, w, eps, y, rstd)
     bd, dx, dg, dw = _bwd_desc(dy, x, g, w, rstd, dx, dg, dw, dw_fp32, deterministic,
                                workspace_buf)
-    with torch.cuda.device(x.device):
+    with _on(x.device):
         st = lib.gnorm_ckpt_step_ex(ctypes.byref(fd), ctypes.byref(bd),
                                     _stream(stream, x.device))
     _check(st, "gnorm_ckpt_step")
@@ -310,7 +330,7 @@ def gnorm_fwd_bwd(x, g, w, eps: float, dy, *, y=None, rstd=None, dx=None, dg=Non
     fd, y, rstd = _fwd_desc(x, g, w, eps, y, rstd)
     bd, dx, dg, dw = _bwd_desc(dy, x, g, w, rstd, dx, dg, dw, dw_fp32, deterministic,
                                workspace_buf)
-    with torch.cuda.device(x.device):
+    with _on(x.device):
         st = lib.gnorm_fwd_bwd_ex(ctypes.byref(fd), ctypes.byref(bd), _stream(stream, x.device))
     _check(st, "gnorm_fwd_bwd")
     return y, rstd, dx, dg, dw
@@ -415,7 +435,7 @@ def gnorm_bwd_noalloc(dy, x, g, w, rstd, *, dx=None, dg=None, dw=None, dw_fp32: 
         dw = torch.empty(N, dtype=dw_dtype, device=x.device)
     else:
         _vec(dw, N, (dw_dtype,), "dw", x.device)
-    with torch.cuda.device(x.device):
+    with _on(x.device):
         st = lib.gnorm_bwd_noalloc(_ptr(dy), _ptr(x), _ptr(g), _ptr(w), _ptr(rstd), _ptr(dx),
                                    _ptr(dg), _ptr(dw), int(bool(dw_fp32)),
                                    int(bool(deterministic)), M, N, _stream(stream, x.device))
