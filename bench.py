@@ -127,7 +127,7 @@ def measured_peaks():
 # valid.
 _DIGEST_EXCLUDED = ("host_step.cu", "noalloc.cu", "block.cu", "block_kernel.cuh", "delta.cu",
                     "delta_common.cuh", "delta_grad.cuh", "delta_prep.cuh", "delta_scan.cuh",
-                    "delta_step.cuh")
+                    "delta_step.cuh", "tcgen05.cuh")
 
 
 def _code_only(text):

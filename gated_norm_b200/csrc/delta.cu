@@ -316,6 +316,7 @@ int gnorm_delta_bwd(const gnorm_delta_bwd_desc* desc, void* stream) {
   }
   DeviceInfo info;
   if ((st = device_info(&info)) != GNORM_OK) return st;
+  a.err = info.err_word;
   const cudaStream_t s = as_stream(stream);
   const cudaError_t e =
       d.K == 64 ? run_bwd<64>(a, info.num_sms, s) : run_bwd<128>(a, info.num_sms, s);

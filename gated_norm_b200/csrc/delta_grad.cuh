@@ -16,41 +16,70 @@
 //
 // One CTA per (chunk, key head) goes through the value heads of the group and adds their dQ
 // and dK in registers, so the sum over shared heads has a fixed order.
+//
+// Everything here is products of 64-token tiles, done by tcgen05.  An instruction has 128
+// rows; the 64 of a query-side product and the 64 of the key-side product with the same right
+// operand are one: [dO; dX] S^T, [dO; dX] W^T, [Q; K] K^T, [Ph; -Eh] K.  Rows 0..63 of every
+// accumulator belong to dQ, rows 64..127 to dK, and where only the key side has a product
+// (W D^T, the transposed Ph and Eh, the second parts of dX and W) the upper rows multiply
+// whatever tile lies before it and are not read.  A thread owns one row and half of the columns.
+// Operands that are not exact in BF16 are in two parts here: dq and dk are BF16.
 #pragma once
 
 #include "delta_common.cuh"
+#include "tcgen05.cuh"
 
 namespace gnorm {
 
 constexpr int kGradThreads = 256;
 constexpr int kMLd = 65;
+constexpr unsigned kErrWaitMma = 8u;  // a wait for the tensor cores ran out
 
 template <int KD, int VD>
 struct GradSmem {
-  static constexpr int kQ = 0;
-  static constexpr int kK = kQ + KD / 64 * kTileBytes;
-  static constexpr int kDo = kK + KD / 64 * kTileBytes;
-  static constexpr int kXh = kDo + VD / 64 * kTileBytes;
-  static constexpr int kXl = kXh + VD / 64 * kTileBytes;
-  static constexpr int kW = kXl + VD / 64 * kTileBytes;
-  // S, then D (hi and lo tiles); then Ph and Eh + Eh^T (hi and lo) and the pair terms
-  static constexpr int kBig = kW + 2 * (VD / 64) * kTileBytes;
+  // [q][k] of each 64 columns of K, then [do][dX hi][dX lo][W hi][W lo] of each 64 columns of V
+  static constexpr int kQK = 0;
+  static constexpr int kA = kQK + KD / 64 * 2 * kTileBytes;
+  // S, then D (hi and lo tiles); then Ph, -Eh (hi, then lo) and the pair terms' running sums
+  static constexpr int kBig = kA + VD / 64 * 5 * kTileBytes;
   static constexpr int kState = 2 * (VD / 64) * (KD / 64) * kTileBytes;
-  static constexpr int kPairs = 4 * kTileBytes + 64 * kMLd * 4;
+  static constexpr int kPairs = 4 * kTileBytes + 128 * kMLd * 4;
   static constexpr int kScal = kBig + (kState > kPairs ? kState : kPairs);
-  static constexpr int kBytes = kScal + 4096;
+  static constexpr int kBytes = kScal + 5120 + 1024;  // 1024: the tiles' alignment
 };
 
 template <int KD, int VD>
 __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __grid_constant__ DeltaArgs a) {
   using L = GradSmem<KD, VD>;
-  extern __shared__ __align__(128) uint8_t smem[];
-  constexpr int kNT = KD / 16;  // 8-column tiles of a warp's half of K
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
   constexpr int kVT = VD / 64, kKT = KD / 64;
+  constexpr int kHalf = KD / 2;                         // columns of K per thread
+  constexpr int kF4 = KD * VD / 4 / kGradThreads;       // float4 of a state per thread
+  // tensor memory columns (the second use of a range follows the reads of the first)
+  constexpr uint32_t kD1 = 0, kD5 = 0;                  // [dO; dX] S^T     | [-; Ph^T] Q - [-; Eh^T] K
+  constexpr uint32_t kD3 = 128, kD2b = 128;             // [-; dX lo] W^T   | [-; W] D^T
+  constexpr uint32_t kD4 = 256, kD1b = 256;             // [-; dX lo] S^T   | [Ph; -Eh] K
+  constexpr uint32_t kD2 = 384, kKK = 448;              // [dO; dX] W^T,  [Q; K] K^T
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int mw = warp & 3, nw = warp >> 2;  // 16 tokens, half of the columns
+  const int row = (warp & 3) * 32 + lane;               // 0..63 dQ, 64..127 dK
+  const int half = warp >> 2;
+  const bool key_side = (warp & 2) != 0;
+  const int tok = row & 63;
   const long long slot = blockIdx.x;
   const int hk = blockIdx.y;
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t s0 = smem_u32(smem);
+  double* Gs = reinterpret_cast<double*>(smem + L::kScal);          // [64]
+  float* scal = reinterpret_cast<float*>(smem + L::kScal + 512);    // beta, gamma, lambda, e^{G_C}
+  float* adot = scal + 256;                                         // [4][64]
+  float* bsum = adot + 256;                                         // [64]
+  float* dbs = bsum + 64;                                           // [64]
+  float* vpart = dbs + 64;                                          // [4][64]
+  float* red = vpart + 256;                                         // [8]
+  float* rowsum = red + 8;                                          // [128]
+  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::kScal + 5096);
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + L::kScal + 5104);
+
   grid_dependency_wait();
   allow_dependent_launch();
   const int b = seq_of_slot(a.seq, slot, lane);
@@ -59,23 +88,34 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
   const long long left = seq_end(a.seq, b) - t0;
   if (b == a.seq.B || chunk < 0 || left <= 0) return;
   const int live = static_cast<int>(left < kChunk ? left : kChunk);
-  const uint32_t s0 = smem_u32(smem);
-  double* Gs = reinterpret_cast<double*>(smem + L::kScal);          // [64]
-  float* scal = reinterpret_cast<float*>(smem + L::kScal + 512);    // beta, gamma, lambda, e^{G_C}
-  float* adot = scal + 256;                                         // [2][64]
-  float* bsum = adot + 128;                                         // [64]
-  float* dbs = bsum + 64;                                           // [64]
-  float* red = dbs + 64;                                            // [8]
-  const int i0 = mw * 16;
-  const int ra = i0 + (lane >> 2), rb = ra + 8;
+  if (warp == 0) tmem_alloc(tslot, 512);
+  if (tid == 32) {
+    mbar_init(bar, 1);
+    fence_barrier_init();
+  }
+#pragma unroll
+  for (int kt = 0; kt < kKT; ++kt) {
+    const long long col = static_cast<long long>(hk) * KD + kt * 64;
+    load_rows<kGradThreads>(s0 + L::kQK + kt * 2 * kTileBytes, a.q + t0 * a.ldq + col, a.ldq, 64, live, tid);
+    load_rows<kGradThreads>(s0 + L::kQK + (kt * 2 + 1) * kTileBytes, a.k + t0 * a.ldk + col, a.ldk, 64, live, tid);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tslot;
+  const uint32_t mine = tmem + (static_cast<uint32_t>(warp & 3) << 21);  // this warp's lanes
+  const uint32_t aA = s0 + L::kA, big = s0 + L::kBig;
+  uint32_t phase = 0;
+  bool alive = true;
+  auto wait_mma = [&]() {
+    if (alive) alive = mbar_wait(bar, phase, a.err, kErrWaitMma);
+    phase ^= 1u;
+    tc_fence_after();
+  };
 
-  load_rows<kGradThreads>(s0 + L::kQ, a.q + t0 * a.ldq + static_cast<long long>(hk) * KD, a.ldq, KD, live, tid);
-  load_rows<kGradThreads>(s0 + L::kK, a.k + t0 * a.ldk + static_cast<long long>(hk) * KD, a.ldk, KD, live, tid);
-  float dq[kNT][4], dk[kNT][4];
+  float acc[kHalf];  // dQ or dK of this row
 #pragma unroll
-  for (int n = 0; n < kNT; ++n)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) dq[n][e] = dk[n][e] = 0.f;
+  for (int i = 0; i < kHalf; ++i) acc[i] = 0.f;
 
   const int group = a.Hv / a.Hk;
   for (int r = 0; r < group; ++r) {
@@ -83,31 +123,21 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
     const long long hs = slot * a.Hv + h;
     const float4* S4 = reinterpret_cast<const float4*>(a.s_ws + hs * KD * VD * 4);
     const float4* D4 = reinterpret_cast<const float4*>(a.d_ws + hs * KD * VD * 4);
-    load_rows<kGradThreads>(s0 + L::kDo, a.dout + t0 * a.lddo + static_cast<long long>(h) * VD, a.lddo, VD, live, tid);
-    load_rows<kGradThreads>(s0 + L::kXh, a.dv + t0 * a.lddv + static_cast<long long>(h) * VD, a.lddv, VD, live, tid);
-    load_flat<kGradThreads>(s0 + L::kXl, a.x_ws + hs * (kVT * kTileBytes), kVT * kTileBytes, tid);
-    load_flat<kGradThreads>(s0 + L::kW, a.w_ws + hs * (3 * kVT * kTileBytes), 2 * kVT * kTileBytes, tid);
+    float4 sv[kF4];
+#pragma unroll
+    for (int i = 0; i < kF4; ++i) sv[i] = S4[tid + i * kGradThreads];
+#pragma unroll
+    for (int vt = 0; vt < kVT; ++vt) {
+      const uint32_t at = aA + vt * 5 * kTileBytes;
+      const long long col = static_cast<long long>(h) * VD + vt * 64;
+      load_rows<kGradThreads>(at, a.dout + t0 * a.lddo + col, a.lddo, 64, live, tid);
+      load_rows<kGradThreads>(at + kTileBytes, a.dv + t0 * a.lddv + col, a.lddv, 64, live, tid);
+      load_flat<kGradThreads>(at + 2 * kTileBytes, a.x_ws + (hs * kVT + vt) * kTileBytes, kTileBytes, tid);
+      const uint8_t* w = a.w_ws + (hs * 3 * kVT + vt) * kTileBytes;
+      load_flat<kGradThreads>(at + 3 * kTileBytes, w, kTileBytes, tid);
+      load_flat<kGradThreads>(at + 4 * kTileBytes, w + kVT * kTileBytes, kTileBytes, tid);
+    }
     cp_commit();
-    // a state in fragment order -> hi and lo tiles [v][k]
-    auto state_tiles = [&](const float4* src) {
-#pragma unroll 4
-      for (int f = tid; f < KD * VD / 4; f += kGradThreads) {
-        const float4 x = src[f];
-        const int ln = f & 31, n = (f >> 5) % (KD / 8), strip = (f >> 5) / (KD / 8);
-        const int v = strip * 16 + (ln >> 2);
-        uint32_t off = ((v >> 6) * kKT + (n >> 3)) * kTileBytes + tile_off(v & 63, n & 7) + (ln & 3) * 4;
-        uint32_t hi, lo;
-        uint8_t* big = smem + L::kBig;
-        split2(x.x, x.y, hi, lo);
-        *reinterpret_cast<uint32_t*>(big + off) = hi;
-        *reinterpret_cast<uint32_t*>(big + L::kState / 2 + off) = lo;
-        off = ((v >> 6) * kKT + (n >> 3)) * kTileBytes + tile_off((v & 63) + 8, n & 7) + (ln & 3) * 4;
-        split2(x.z, x.w, hi, lo);
-        *reinterpret_cast<uint32_t*>(big + off) = hi;
-        *reinterpret_cast<uint32_t*>(big + L::kState / 2 + off) = lo;
-      }
-    };
-    state_tiles(S4);
     if (warp == 0) {
       const int ta = 2 * lane, tb = ta + 1;
       const float ga = ta < live ? clamp_decay(a.g[(t0 + ta) * a.ldg + h]) : 0.f;
@@ -133,294 +163,229 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
         (which == 0 ? bsum : dbs)[t] = v;
       }
     }
+    // a state in fragment order -> hi and lo tiles [v][k]
+    auto state_tiles = [&](const float4* x) {
+#pragma unroll
+      for (int i = 0; i < kF4; ++i) {
+        const int f = tid + i * kGradThreads;
+        const int ln = f & 31, n = (f >> 5) % (KD / 8), strip = (f >> 5) / (KD / 8);
+        const int v = strip * 16 + (ln >> 2);
+        uint8_t* dst = smem + L::kBig + ((v >> 6) * kKT + (n >> 3)) * kTileBytes + (ln & 3) * 4;
+        uint32_t hi, lo;
+        split2(x[i].x, x[i].y, hi, lo);
+        *reinterpret_cast<uint32_t*>(dst + tile_off(v & 63, n & 7)) = hi;
+        *reinterpret_cast<uint32_t*>(dst + L::kState / 2 + tile_off(v & 63, n & 7)) = lo;
+        split2(x[i].z, x[i].w, hi, lo);
+        *reinterpret_cast<uint32_t*>(dst + tile_off((v & 63) + 8, n & 7)) = hi;
+        *reinterpret_cast<uint32_t*>(dst + L::kState / 2 + tile_off((v & 63) + 8, n & 7)) = lo;
+      }
+    };
+    state_tiles(sv);
     cp_wait<0>();
+    fence_smem_to_async();
+    tc_fence_before();
     __syncthreads();
-
-    const float ga = scal[64 + ra], gb = scal[64 + rb];
-    // ---- products with S: dO S^T and dX S^T
-    {
-      float acc[kNT][4], acc2[kNT][4];
+    if (tid == 0) {
+      tc_fence_after();
+      constexpr uint32_t idS = mma_desc<false, true, KD>(), idW = mma_desc<false, false, 64>();
 #pragma unroll
-      for (int n = 0; n < kNT; ++n)
+      for (int ks = 0; ks < VD / 16; ++ks) {
+        const uint32_t at = aA + (ks >> 2) * 5 * kTileBytes + (ks & 3) * 32;
+        const uint64_t a0 = smem_desc(at, 16, 1024), a1 = smem_desc(at + kTileBytes, 16, 1024);
+        const uint32_t st = big + (ks >> 2) * kKT * kTileBytes + (ks & 3) * 2048;
+        const uint64_t sh = smem_desc(st, kTileBytes, 1024);
+        const uint64_t sl = smem_desc(st + L::kState / 2, kTileBytes, 1024);
+        const uint64_t wh = smem_desc(at + 3 * kTileBytes, 16, 1024);
+        const uint64_t wl = smem_desc(at + 4 * kTileBytes, 16, 1024);
+        tc_mma(tmem + kD1, a0, sh, idS, ks > 0);
+        tc_mma(tmem + kD1, a0, sl, idS, true);
+        tc_mma(tmem + kD1b, a1, sh, idS, ks > 0);
+        tc_mma(tmem + kD2, a0, wh, idW, ks > 0);
+        tc_mma(tmem + kD2, a0, wl, idW, true);
+        tc_mma(tmem + kD2b, a1, wh, idW, ks > 0);
+      }
+      if (r == 0) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[n][e] = acc2[n][e] = 0.f;
-#pragma unroll
-      for (int kb = 0; kb < VD / 16; ++kb) {
-        const uint32_t toff = (kb >> 2) * kTileBytes;
-        const int c0 = (kb & 3) * 16;
-        uint32_t ao[4], xh[4], xl[4];
-        ldsm4(ao, addr_a(s0 + L::kDo + toff, i0, c0, lane));
-        ldsm4(xh, addr_a(s0 + L::kXh + toff, i0, c0, lane));
-        ldsm4(xl, addr_a(s0 + L::kXl + toff, i0, c0, lane));
-#pragma unroll
-        for (int nb = 0; nb < kNT / 2; ++nb) {
-          const int col = nw * (KD / 2) + nb * 16;
-          const uint32_t tile = s0 + L::kBig + ((kb >> 2) * kKT + (col >> 6)) * kTileBytes;
-          uint32_t bh[4], bl[4];
-          ldsm4t(bh, addr_bt(tile, c0, col & 63, lane));
-          ldsm4t(bl, addr_bt(tile + L::kState / 2, c0, col & 63, lane));
-          mma16816(acc[2 * nb], ao, bh[0], bh[1]);
-          mma16816(acc[2 * nb + 1], ao, bh[2], bh[3]);
-          mma16816(acc2[2 * nb], xh, bh[0], bh[1]);
-          mma16816(acc2[2 * nb + 1], xh, bh[2], bh[3]);
-          mma16816(acc[2 * nb], ao, bl[0], bl[1]);
-          mma16816(acc[2 * nb + 1], ao, bl[2], bl[3]);
-          mma16816(acc2[2 * nb], xl, bh[0], bh[1]);
-          mma16816(acc2[2 * nb + 1], xl, bh[2], bh[3]);
-          mma16816(acc2[2 * nb], xh, bl[0], bl[1]);
-          mma16816(acc2[2 * nb + 1], xh, bl[2], bl[3]);
+        for (int ks = 0; ks < KD / 16; ++ks) {
+          const uint32_t at = s0 + L::kQK + (ks >> 2) * 2 * kTileBytes + (ks & 3) * 32;
+          tc_mma(tmem + kKK, smem_desc(at, 16, 1024), smem_desc(at + kTileBytes, 16, 1024), idW, ks > 0);
         }
       }
-      // scale the rows, add, and the rows' products with q and k (a_i)
-      float da = 0.f, db = 0.f;
-#pragma unroll
-      for (int n = 0; n < kNT; ++n) {
-        const int col = nw * (KD / 2) + n * 8;
-        const uint32_t oa = (col >> 6) * kTileBytes + tile_off(ra, (col & 63) >> 3) + (lane & 3) * 4;
-        const uint32_t ob = (col >> 6) * kTileBytes + tile_off(rb, (col & 63) >> 3) + (lane & 3) * 4;
-        const uint32_t qa = *reinterpret_cast<const uint32_t*>(smem + L::kQ + oa);
-        const uint32_t qb = *reinterpret_cast<const uint32_t*>(smem + L::kQ + ob);
-        const uint32_t ka = *reinterpret_cast<const uint32_t*>(smem + L::kK + oa);
-        const uint32_t kb2 = *reinterpret_cast<const uint32_t*>(smem + L::kK + ob);
-        const float sa = a.scale * ga, sb = a.scale * gb;
-        acc[n][0] *= sa;
-        acc[n][1] *= sa;
-        acc[n][2] *= sb;
-        acc[n][3] *= sb;
-        acc2[n][0] *= -ga;
-        acc2[n][1] *= -ga;
-        acc2[n][2] *= -gb;
-        acc2[n][3] *= -gb;
-        da += acc[n][0] * bf_lo(qa) + acc[n][1] * bf_hi(qa) + acc2[n][0] * bf_lo(ka) + acc2[n][1] * bf_hi(ka);
-        db += acc[n][2] * bf_lo(qb) + acc[n][3] * bf_hi(qb) + acc2[n][2] * bf_lo(kb2) + acc2[n][3] * bf_hi(kb2);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          dq[n][e] += acc[n][e];
-          dk[n][e] += acc2[n][e];
-        }
-      }
-      da += __shfl_xor_sync(0xffffffffu, da, 1);
-      da += __shfl_xor_sync(0xffffffffu, da, 2);
-      db += __shfl_xor_sync(0xffffffffu, db, 1);
-      db += __shfl_xor_sync(0xffffffffu, db, 2);
-      if ((lane & 3) == 0) {
-        adot[nw * 64 + ra] = da;
-        adot[nw * 64 + rb] = db;
-      }
+      tc_commit(bar);
     }
-    __syncthreads();
-    // ---- D takes S's place; <S, D>
-    state_tiles(D4);
+    // meanwhile D, and <S, D>
+    float4 dv4[kF4];
+#pragma unroll
+    for (int i = 0; i < kF4; ++i) dv4[i] = D4[tid + i * kGradThreads];
     {
       float v = 0.f;
-#pragma unroll 4
-      for (int f = tid; f < KD * VD / 4; f += kGradThreads) {
-        const float4 x = S4[f], y = D4[f];
-        v += x.x * y.x + x.y * y.y + x.z * y.z + x.w * y.w;
-      }
+#pragma unroll
+      for (int i = 0; i < kF4; ++i)
+        v += sv[i].x * dv4[i].x + sv[i].y * dv4[i].y + sv[i].z * dv4[i].z + sv[i].w * dv4[i].w;
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
       if (lane == 0) red[warp] = v;
     }
+    wait_mma();
+    // ---- D takes S's place
+    state_tiles(dv4);
+    // E (key side) or F, and the second part of E before its range is used again
+    float ef[32];
+    tc_load32(mine + kD2 + half * 32, ef);
+    if (key_side) {
+      float t[32];
+      tc_load32(mine + kD2b + half * 32, t);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) ef[i] += t[i];
+    }
+    fence_smem_to_async();
+    tc_fence_before();
     __syncthreads();
-    // ---- lambda beta W D^T
+    if (tid == 0) {
+      tc_fence_after();
+      constexpr uint32_t idS = mma_desc<false, true, KD>();
+#pragma unroll
+      for (int ks = 0; ks < VD / 16; ++ks) {
+        const uint32_t at = aA + (ks >> 2) * 5 * kTileBytes + (ks & 3) * 32;
+        const uint32_t st = big + (ks >> 2) * kKT * kTileBytes + (ks & 3) * 2048;
+        const uint64_t wh = smem_desc(at + 2 * kTileBytes, 16, 1024);  // rows 64..127: W hi
+        const uint64_t wl = smem_desc(at + 3 * kTileBytes, 16, 1024);
+        const uint64_t dh = smem_desc(st, kTileBytes, 1024);
+        const uint64_t dl = smem_desc(st + L::kState / 2, kTileBytes, 1024);
+        tc_mma(tmem + kD3, wh, dh, idS, ks > 0);
+        tc_mma(tmem + kD3, wh, dl, idS, true);
+        tc_mma(tmem + kD3, wl, dh, idS, true);
+      }
+      tc_commit(bar);
+    }
+    // ---- meanwhile the products with S: scale the row, add, and its product with q or k (a_i)
     {
-      float acc[kNT][4];
+      const float f = key_side ? -scal[64 + tok] : a.scale * scal[64 + tok];
+      float dot = 0.f;
 #pragma unroll
-      for (int n = 0; n < kNT; ++n)
+      for (int c = 0; c < kHalf / 32; ++c) {
+        float t[32];
+        tc_load32(mine + kD1 + half * kHalf + c * 32, t);
+        if (key_side) {
+          float u[32];
+          tc_load32(mine + kD1b + half * kHalf + c * 32, u);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
-#pragma unroll
-      for (int kb = 0; kb < VD / 16; ++kb) {
-        const uint32_t toff = (kb >> 2) * kTileBytes;
-        const int c0 = (kb & 3) * 16;
-        uint32_t wh[4], wl[4];
-        ldsm4(wh, addr_a(s0 + L::kW + toff, i0, c0, lane));
-        ldsm4(wl, addr_a(s0 + L::kW + kVT * kTileBytes + toff, i0, c0, lane));
-#pragma unroll
-        for (int nb = 0; nb < kNT / 2; ++nb) {
-          const int col = nw * (KD / 2) + nb * 16;
-          const uint32_t tile = s0 + L::kBig + ((kb >> 2) * kKT + (col >> 6)) * kTileBytes;
-          uint32_t bh[4], bl[4];
-          ldsm4t(bh, addr_bt(tile, c0, col & 63, lane));
-          ldsm4t(bl, addr_bt(tile + L::kState / 2, c0, col & 63, lane));
-          mma16816(acc[2 * nb], wh, bh[0], bh[1]);
-          mma16816(acc[2 * nb + 1], wh, bh[2], bh[3]);
-          mma16816(acc[2 * nb], wl, bh[0], bh[1]);
-          mma16816(acc[2 * nb + 1], wl, bh[2], bh[3]);
-          mma16816(acc[2 * nb], wh, bl[0], bl[1]);
-          mma16816(acc[2 * nb + 1], wh, bl[2], bl[3]);
+          for (int i = 0; i < 32; ++i) t[i] += u[i];
         }
-      }
-      const float fa = scal[128 + ra] * scal[ra], fb = scal[128 + rb] * scal[rb];
+        const int col = half * kHalf + c * 32;
+        const uint8_t* src = smem + L::kQK + ((col >> 6) * 2 + (key_side ? 1 : 0)) * kTileBytes;
 #pragma unroll
-      for (int n = 0; n < kNT; ++n) {
-        dk[n][0] = fmaf(fa, acc[n][0], dk[n][0]);
-        dk[n][1] = fmaf(fa, acc[n][1], dk[n][1]);
-        dk[n][2] = fmaf(fb, acc[n][2], dk[n][2]);
-        dk[n][3] = fmaf(fb, acc[n][3], dk[n][3]);
-      }
-    }
-    // ---- E, F, K K^T, Q K^T: rows i0.., columns 32 nw .. +31
-    float E[4][4], F[4][4], kk[4][4], qk[4][4];
+        for (int p = 0; p < 4; ++p) {
+          const uint4 x = *reinterpret_cast<const uint4*>(src + tile_off(tok, ((col & 63) >> 3) + p));
+          float xf[8];
+          bf16x8_to_f32(x, xf);
 #pragma unroll
-    for (int n = 0; n < 4; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) E[n][e] = F[n][e] = kk[n][e] = qk[n][e] = 0.f;
-#pragma unroll
-    for (int kb = 0; kb < VD / 16; ++kb) {
-      const uint32_t toff = (kb >> 2) * kTileBytes;
-      const int c0 = (kb & 3) * 16;
-      uint32_t ao[4], xh[4], xl[4];
-      ldsm4(ao, addr_a(s0 + L::kDo + toff, i0, c0, lane));
-      ldsm4(xh, addr_a(s0 + L::kXh + toff, i0, c0, lane));
-      ldsm4(xl, addr_a(s0 + L::kXl + toff, i0, c0, lane));
-#pragma unroll
-      for (int nb = 0; nb < 2; ++nb) {
-        uint32_t bh[4], bl[4];
-        ldsm4(bh, addr_b(s0 + L::kW + toff, nw * 32 + nb * 16, c0, lane));
-        ldsm4(bl, addr_b(s0 + L::kW + kVT * kTileBytes + toff, nw * 32 + nb * 16, c0, lane));
-        mma16816(F[2 * nb], ao, bh[0], bh[1]);
-        mma16816(F[2 * nb + 1], ao, bh[2], bh[3]);
-        mma16816(E[2 * nb], xh, bh[0], bh[1]);
-        mma16816(E[2 * nb + 1], xh, bh[2], bh[3]);
-        mma16816(F[2 * nb], ao, bl[0], bl[1]);
-        mma16816(F[2 * nb + 1], ao, bl[2], bl[3]);
-        mma16816(E[2 * nb], xl, bh[0], bh[1]);
-        mma16816(E[2 * nb + 1], xl, bh[2], bh[3]);
-        mma16816(E[2 * nb], xh, bl[0], bl[1]);
-        mma16816(E[2 * nb + 1], xh, bl[2], bl[3]);
-      }
-    }
-#pragma unroll
-    for (int kb = 0; kb < KD / 16; ++kb) {
-      const uint32_t toff = (kb >> 2) * kTileBytes;
-      const int c0 = (kb & 3) * 16;
-      uint32_t ak[4], aq[4];
-      ldsm4(ak, addr_a(s0 + L::kK + toff, i0, c0, lane));
-      ldsm4(aq, addr_a(s0 + L::kQ + toff, i0, c0, lane));
-#pragma unroll
-      for (int nb = 0; nb < 2; ++nb) {
-        uint32_t bk[4];
-        ldsm4(bk, addr_b(s0 + L::kK + toff, nw * 32 + nb * 16, c0, lane));
-        mma16816(kk[2 * nb], ak, bk[0], bk[1]);
-        mma16816(kk[2 * nb + 1], ak, bk[2], bk[3]);
-        mma16816(qk[2 * nb], aq, bk[0], bk[1]);
-        mma16816(qk[2 * nb + 1], aq, bk[2], bk[3]);
-      }
-    }
-    __syncthreads();  // D has been read: its place takes the pair tiles
-    uint8_t* ph = smem + L::kBig;  // Ph hi, lo, Eh + Eh^T hi, lo
-    float* M = reinterpret_cast<float*>(ph + 4 * kTileBytes);
-    {
-      const double Ga = Gs[ra], Gb = Gs[rb];
-#pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const int c = nw * 32 + n * 8 + 2 * (lane & 3);
-        float p[4], x[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int i = e < 2 ? ra : rb, j = c + (e & 1);
-          const double G = e < 2 ? Ga : Gb;
-          const float d = j <= i ? expf(static_cast<float>(G - Gs[j])) * scal[j] : 0.f;
-          p[e] = j <= i ? a.scale * F[n][e] * d : 0.f;
-          x[e] = j < i ? E[n][e] * d : 0.f;
-          M[i * kMLd + j] = j < i ? p[e] * qk[n][e] - x[e] * kk[n][e] : 0.f;
-        }
-        uint32_t hi, lo;
-        const uint32_t oa = tile_off(ra, c >> 3) + (c & 7) * 2, ob = tile_off(rb, c >> 3) + (c & 7) * 2;
-        split2(p[0], p[1], hi, lo);
-        *reinterpret_cast<uint32_t*>(ph + oa) = hi;
-        *reinterpret_cast<uint32_t*>(ph + kTileBytes + oa) = lo;
-        split2(p[2], p[3], hi, lo);
-        *reinterpret_cast<uint32_t*>(ph + ob) = hi;
-        *reinterpret_cast<uint32_t*>(ph + kTileBytes + ob) = lo;
-        // Eh below the diagonal and its mirror above; each place is written once
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int i = e < 2 ? ra : rb, j = c + (e & 1);
-          if (j <= i) {
-            const __nv_bfloat16 xh = __float2bfloat16_rn(x[e]);
-            const __nv_bfloat16 xl = __float2bfloat16_rn(x[e] - __bfloat162float(xh));
-            const uint32_t oij = tile_off(i, j >> 3) + (j & 7) * 2, oji = tile_off(j, i >> 3) + (i & 7) * 2;
-            *reinterpret_cast<__nv_bfloat16*>(ph + 2 * kTileBytes + oij) = xh;
-            *reinterpret_cast<__nv_bfloat16*>(ph + 3 * kTileBytes + oij) = xl;
-            if (j < i) {
-              *reinterpret_cast<__nv_bfloat16*>(ph + 2 * kTileBytes + oji) = xh;
-              *reinterpret_cast<__nv_bfloat16*>(ph + 3 * kTileBytes + oji) = xl;
-            }
+          for (int e = 0; e < 8; ++e) {
+            const float v = f * t[p * 8 + e];
+            dot = fmaf(v, xf[e], dot);
+            acc[c * 32 + p * 8 + e] += v;
           }
         }
       }
+      adot[(half * 2 + (key_side ? 1 : 0)) * 64 + tok] = dot;
     }
-    __syncthreads();
-    // ---- dQ += Ph K;  dK += Ph^T Q - (Eh + Eh^T) K
+    // ---- the pair terms: this row's 32 columns of Ph or -Eh, and of their products with q.k or k.k
+    uint32_t hi[16], lo[16];
     {
-      float neg[kNT][4];
-#pragma unroll
-      for (int n = 0; n < kNT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) neg[n][e] = 0.f;
-#pragma unroll
-      for (int kb = 0; kb < 4; ++kb) {
-        uint32_t ph4[4], pl4[4], th[4], tl[4], eh[4], el[4];
-        const uint32_t P = s0 + L::kBig;
-        ldsm4(ph4, addr_a(P, i0, kb * 16, lane));
-        ldsm4(pl4, addr_a(P + kTileBytes, i0, kb * 16, lane));
-        ldsm4t(th, addr_at(P, kb * 16, i0, lane));
-        ldsm4t(tl, addr_at(P + kTileBytes, kb * 16, i0, lane));
-        ldsm4(eh, addr_a(P + 2 * kTileBytes, i0, kb * 16, lane));
-        ldsm4(el, addr_a(P + 3 * kTileBytes, i0, kb * 16, lane));
-#pragma unroll
-        for (int nb = 0; nb < kNT / 2; ++nb) {
-          const int col = nw * (KD / 2) + nb * 16;
-          uint32_t bk[4], bq[4];
-          ldsm4t(bk, addr_bt(s0 + L::kK + (col >> 6) * kTileBytes, kb * 16, col & 63, lane));
-          ldsm4t(bq, addr_bt(s0 + L::kQ + (col >> 6) * kTileBytes, kb * 16, col & 63, lane));
-          if (kb <= mw) {
-            mma16816(dq[2 * nb], ph4, bk[0], bk[1]);
-            mma16816(dq[2 * nb + 1], ph4, bk[2], bk[3]);
-            mma16816(dq[2 * nb], pl4, bk[0], bk[1]);
-            mma16816(dq[2 * nb + 1], pl4, bk[2], bk[3]);
-          }
-          if (kb >= mw) {
-            mma16816(dk[2 * nb], th, bq[0], bq[1]);
-            mma16816(dk[2 * nb + 1], th, bq[2], bq[3]);
-            mma16816(dk[2 * nb], tl, bq[0], bq[1]);
-            mma16816(dk[2 * nb + 1], tl, bq[2], bq[3]);
-          }
-          mma16816(neg[2 * nb], eh, bk[0], bk[1]);
-          mma16816(neg[2 * nb + 1], eh, bk[2], bk[3]);
-          mma16816(neg[2 * nb], el, bk[0], bk[1]);
-          mma16816(neg[2 * nb + 1], el, bk[2], bk[3]);
-        }
-      }
-#pragma unroll
-      for (int n = 0; n < kNT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) dk[n][e] -= neg[n][e];
-    }
-    // ---- dg and dbeta.  M's rows become their running sums over j < t, then column t is
-    // summed over i >= t.
-    if (tid < 64) {
-      float* row = M + tid * kMLd;
+      float kk[32];
+      tc_load32(mine + kKK + half * 32, kk);
+      const double G = Gs[tok];
       float run = 0.f;
-#pragma unroll 8
-      for (int j = 0; j < 64; ++j) {
-        const float m = row[j];
-        row[j] = run;
-        run += m;
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        float p[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int j = half * 32 + i + e;
+          float v = 0.f;
+          if (key_side ? j < tok : j <= tok) {
+            const float d = expf(static_cast<float>(G - Gs[j])) * scal[j];
+            v = key_side ? -ef[i + e] * d : a.scale * ef[i + e] * d;
+          }
+          p[e] = v;
+          // running sums over the columns before, in the place of the terms
+          const float m = j < tok ? v * kk[i + e] : 0.f;
+          ef[i + e] = run;
+          run += m;
+        }
+        split2(p[0], p[1], hi[i / 2], lo[i / 2]);
       }
+      if (half == 0) rowsum[row] = run;
+    }
+    wait_mma();  // W D^T is done, its tiles' place is free
+    {
+      uint8_t* dst = smem + L::kBig + (key_side ? kTileBytes : 0);
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        const uint32_t off = tile_off(tok, half * 4 + p);
+        *reinterpret_cast<uint4*>(dst + off) = make_uint4(hi[4 * p], hi[4 * p + 1], hi[4 * p + 2], hi[4 * p + 3]);
+        *reinterpret_cast<uint4*>(dst + 2 * kTileBytes + off) =
+            make_uint4(lo[4 * p], lo[4 * p + 1], lo[4 * p + 2], lo[4 * p + 3]);
+      }
+      float* M = reinterpret_cast<float*>(smem + L::kBig + 4 * kTileBytes) + row * kMLd + half * 32;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) M[i] = ef[i];
+    }
+    fence_smem_to_async();
+    tc_fence_before();
+    __syncthreads();
+    if (tid == 0) {
+      tc_fence_after();
+      constexpr uint32_t idP = mma_desc<false, true, KD>(), idT = mma_desc<true, true, KD>();
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) {
+        const uint64_t q = smem_desc(s0 + L::kQK + ks * 2048, 2 * kTileBytes, 1024);
+        const uint64_t k = smem_desc(s0 + L::kQK + kTileBytes + ks * 2048, 2 * kTileBytes, 1024);
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+          const uint32_t ph = big + part * 2 * kTileBytes;
+          tc_mma(tmem + kD4, smem_desc(ph + ks * 32, 16, 1024), k, idP, ks + part > 0);
+          // transposed, as rows 64..127: the tile before is rows 0..63
+          tc_mma(tmem + kD5, smem_desc(ph - kTileBytes + ks * 2048, kTileBytes, 1024), q, idT, ks + part > 0);
+          tc_mma(tmem + kD5, smem_desc(ph + ks * 2048, kTileBytes, 1024), k, idT, true);
+        }
+      }
+      tc_commit(bar);
+    }
+    // ---- meanwhile W D^T, and the sums of dg over i >= t
+    if (key_side) {
+      const float f = scal[128 + tok] * scal[tok];
+#pragma unroll
+      for (int c = 0; c < kHalf / 32; ++c) {
+        float t[32];
+        tc_load32(mine + kD3 + half * kHalf + c * 32, t);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) acc[c * 32 + i] = fmaf(f, t[i], acc[c * 32 + i]);
+      }
+    }
+    {
+      // column t of the running sums: rows i >= t of 32 rows of Ph's or Eh's terms
+      const int t = tid & 63, part = tid >> 6;
+      const int i0 = (part & 1) * 32, r0 = (part >> 1) * 64 + i0;
+      const float* M = reinterpret_cast<const float*>(smem + L::kBig + 4 * kTileBytes) + r0 * kMLd + t;
+      float v = 0.f;
+#pragma unroll 8
+      for (int i = 0; i < 32; ++i) {
+        float x = M[i * kMLd];
+        if (t >= 32) x += rowsum[r0 + i];  // the second half's sums start at the first half's
+        v += i0 + i >= t ? x : 0.f;
+      }
+      vpart[part * 64 + t] = v;
     }
     __syncthreads();
     if (tid < 64) {
-      float v = 0.f, pa = 0.f, pb = 0.f, sd = 0.f;
+      float v = vpart[tid] + vpart[64 + tid] + vpart[128 + tid] + vpart[192 + tid];
+      float pa = 0.f, pb = 0.f, sd = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) sd += red[i];
 #pragma unroll 8
       for (int i = 0; i < 64; ++i) {
-        v += i >= tid ? M[i * kMLd + tid] : 0.f;
-        pa += i >= tid ? adot[i] + adot[64 + i] : 0.f;
+        pa += i >= tid ? (adot[i] + adot[64 + i]) + (adot[128 + i] + adot[192 + i]) : 0.f;
         pb += i < tid ? bsum[i] : 0.f;
       }
       if (tid < live) {
@@ -433,20 +398,30 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
           reinterpret_cast<__nv_bfloat16*>(a.dbeta)[t * a.lddbeta + h] = __float2bfloat16_rn(db);
       }
     }
+    wait_mma();
+#pragma unroll
+    for (int c = 0; c < kHalf / 32; ++c) {
+      float t[32];
+      tc_load32(mine + kD4 + half * kHalf + c * 32, t);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) acc[c * 32 + i] += t[i];
+      if (key_side) {
+        tc_load32(mine + kD5 + half * kHalf + c * 32, t);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) acc[c * 32 + i] += t[i];
+      }
+    }
+    tc_fence_before();
     __syncthreads();
   }
+  if (tok < live) {
+    uint16_t* dst = key_side ? a.dk + (t0 + tok) * a.lddk : a.dq + (t0 + tok) * a.lddq;
+    dst += static_cast<long long>(hk) * KD + half * kHalf;
 #pragma unroll
-  for (int n = 0; n < kNT; ++n) {
-    const long long col = static_cast<long long>(hk) * KD + nw * (KD / 2) + n * 8 + 2 * (lane & 3);
-    if (ra < live) {
-      *reinterpret_cast<uint32_t*>(a.dq + (t0 + ra) * a.lddq + col) = pack_bf16x2(dq[n][0], dq[n][1]);
-      *reinterpret_cast<uint32_t*>(a.dk + (t0 + ra) * a.lddk + col) = pack_bf16x2(dk[n][0], dk[n][1]);
-    }
-    if (rb < live) {
-      *reinterpret_cast<uint32_t*>(a.dq + (t0 + rb) * a.lddq + col) = pack_bf16x2(dq[n][2], dq[n][3]);
-      *reinterpret_cast<uint32_t*>(a.dk + (t0 + rb) * a.lddk + col) = pack_bf16x2(dk[n][2], dk[n][3]);
-    }
+    for (int i = 0; i < kHalf / 8; ++i)
+      *reinterpret_cast<uint4*>(dst + i * 8) = f32x8_to_bf16(acc + i * 8);
   }
+  if (warp == 0) tmem_free(tmem, 512);
 }
 
 }  // namespace gnorm

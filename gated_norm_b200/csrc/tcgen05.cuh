@@ -1,0 +1,89 @@
+// tcgen05.cuh -- the fifth-generation tensor cores (sm_100a) as the gated delta rule's gradient
+// kernel uses them: one CTA, BF16 operands in shared memory, FP32 accumulators in tensor
+// memory, 128 rows an instruction.
+#pragma once
+
+#include "device_common.cuh"
+
+namespace gnorm {
+
+// Tensor memory: 128 lanes of 512 columns of 32 bits.  One warp allocates (the base goes to
+// shared memory) and the same warp frees.
+__device__ __forceinline__ void tmem_alloc(uint32_t* smem_slot, uint32_t columns) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                   smem_u32(smem_slot)),
+               "r"(columns)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+}
+__device__ __forceinline__ void tmem_free(uint32_t base, uint32_t columns) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(columns));
+}
+
+// Order against barriers: before a barrier that lets another thread's tensor-core work follow
+// this thread's, and after one that this thread's work is to follow.
+__device__ __forceinline__ void tc_fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+// Makes this thread's shared-memory writes visible to the tensor cores.
+__device__ __forceinline__ void fence_smem_to_async() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// Descriptor of an operand made of 64 x 64 BF16 tiles in the layout of tile_off (rows of 128
+// bytes, 16-byte pieces swizzled over eight rows; tiles 1024-byte aligned): `sbo` bytes from
+// eight rows to the next, `lbo` bytes from 64 columns to the next where the columns are the
+// operand's rows or columns (MN-major; not used otherwise).
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+  return static_cast<uint64_t>((addr & 0x3ffffu) >> 4) |
+         (static_cast<uint64_t>((lbo >> 4) & 0x3fffu) << 16) |
+         (static_cast<uint64_t>((sbo >> 4) & 0x3fffu) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// Instruction descriptor: FP32 += BF16 x BF16, M = 128, N columns; kA / kB: the operand's tiles
+// have the reduction along their rows (MN-major) instead of along their columns.
+template <bool kA, bool kB, int N>
+GNORM_HD constexpr uint32_t mma_desc() {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (kA ? 1u << 15 : 0u) | (kB ? 1u << 16 : 0u) |
+         (static_cast<uint32_t>(N / 8) << 17) | (8u << 24);
+}
+
+// D (tensor memory) = or += A B, 16 of the reduction.  Issued by one thread.
+__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+      : "memory");
+}
+// Arrives on `bar` when all tensor-core work this thread has issued is done.
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                   smem_u32(bar))
+               : "memory");
+}
+
+// 32 columns of this warp's 32 lanes (lane = row); tc_load_wait before the values are used.
+__device__ __forceinline__ void tc_load32(uint32_t addr, float v[32]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,"
+      "%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+}  // namespace gnorm
