@@ -52,6 +52,11 @@ __device__ __forceinline__ void ldsm4t(uint32_t r[4], uint32_t addr) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr));
 }
+__device__ __forceinline__ void stsm4(uint32_t addr, const uint32_t r[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+               : "memory");
+}
 __device__ __forceinline__ void stsm4t(uint32_t addr, const uint32_t r[4]) {
   asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr),
                "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
@@ -224,6 +229,18 @@ __device__ __forceinline__ float load_beta(const DeltaArgs& a, long long tok, in
                            static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(a.beta)[i]) << 16);
 }
 __device__ __forceinline__ float clamp_decay(float g) { return g < kMinLogDecay ? kMinLogDecay : g; }
+
+// The running sum of g inside a chunk as two FP32 values in units of log2: differences of far
+// terms keep their digits without FP64 in the inner loops.
+__device__ __forceinline__ float2 decay_sum(double G) {
+  const double x = G * 1.4426950408889634;
+  const float hi = static_cast<float>(x);
+  return make_float2(hi, static_cast<float>(x - static_cast<double>(hi)));
+}
+// e^{G_i - G_j}
+__device__ __forceinline__ float decay_between(float2 i, float2 j) {
+  return exp2f((i.x - j.x) + (i.y - j.y));
+}
 
 // Copies `live` rows of `cols` (a multiple of 64) BF16 values into swizzled tiles (one per 64
 // columns), zero below; kThreads threads take part.

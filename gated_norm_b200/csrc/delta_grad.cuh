@@ -22,7 +22,7 @@
 // operand are one: [dO; dX] S^T, [dO; dX] W^T, [Q; K] K^T, [Ph; -Eh] K.  Rows 0..63 of every
 // accumulator belong to dQ, rows 64..127 to dK, and where only the key side has a product
 // (W D^T, the transposed Ph and Eh, the second parts of dX and W) the upper rows multiply
-// whatever tile lies before it and are not read.  A thread owns one row and half of the columns.
+// whatever tile lies before it and are not read.  A thread owns one row and a quarter of the columns.
 // Operands that are not exact in BF16 are in two parts here: dq and dk are BF16.
 #pragma once
 
@@ -31,9 +31,10 @@
 
 namespace gnorm {
 
-constexpr int kGradThreads = 256;
+constexpr int kGradThreads = 512;
 constexpr int kMLd = 65;
 constexpr unsigned kErrWaitMma = 8u;  // a wait for the tensor cores ran out
+constexpr int kGradScal = 9216;
 
 template <int KD, int VD>
 struct GradSmem {
@@ -45,7 +46,7 @@ struct GradSmem {
   static constexpr int kState = 2 * (VD / 64) * (KD / 64) * kTileBytes;
   static constexpr int kPairs = 4 * kTileBytes + 128 * kMLd * 4;
   static constexpr int kScal = kBig + (kState > kPairs ? kState : kPairs);
-  static constexpr int kBytes = kScal + 5120 + 1024;  // 1024: the tiles' alignment
+  static constexpr int kBytes = kScal + kGradScal + 1024;  // 1024: the tiles' alignment
 };
 
 template <int KD, int VD>
@@ -53,8 +54,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
   using L = GradSmem<KD, VD>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   constexpr int kVT = VD / 64, kKT = KD / 64;
-  constexpr int kHalf = KD / 2;                         // columns of K per thread
-  constexpr int kF4 = KD * VD / 4 / kGradThreads;       // float4 of a state per thread
+  constexpr int kCols = KD / 4;                         // columns of K per thread
+  constexpr int kPair = KD * VD / 8 / kGradThreads;     // pairs of a state's float4 per thread
   // tensor memory columns (the second use of a range follows the reads of the first)
   constexpr uint32_t kD1 = 0, kD5 = 0;                  // [dO; dX] S^T     | [-; Ph^T] Q - [-; Eh^T] K
   constexpr uint32_t kD3 = 128, kD2b = 128;             // [-; dX lo] W^T   | [-; W] D^T
@@ -62,23 +63,24 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
   constexpr uint32_t kD2 = 384, kKK = 448;              // [dO; dX] W^T,  [Q; K] K^T
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int row = (warp & 3) * 32 + lane;               // 0..63 dQ, 64..127 dK
-  const int half = warp >> 2;
+  const int cq = warp >> 2;                             // quarter of the columns
   const bool key_side = (warp & 2) != 0;
   const int tok = row & 63;
   const long long slot = blockIdx.x;
   const int hk = blockIdx.y;
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t s0 = smem_u32(smem);
-  double* Gs = reinterpret_cast<double*>(smem + L::kScal);          // [64]
+  float2* Gs = reinterpret_cast<float2*>(smem + L::kScal);          // [64]
   float* scal = reinterpret_cast<float*>(smem + L::kScal + 512);    // beta, gamma, lambda, e^{G_C}
-  float* adot = scal + 256;                                         // [4][64]
-  float* bsum = adot + 256;                                         // [64]
+  float* bsum = scal + 256;                                         // [64]
   float* dbs = bsum + 64;                                           // [64]
-  float* vpart = dbs + 64;                                          // [4][64]
-  float* red = vpart + 256;                                         // [8]
-  float* rowsum = red + 8;                                          // [128]
-  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::kScal + 5096);
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + L::kScal + 5104);
+  float* adot = dbs + 64;                                           // [8][64]
+  float* vpart = adot + 512;                                        // [8][64]
+  float* rowsum = vpart + 512;                                      // [4][128]
+  float* red = rowsum + 512;                                        // [16]
+  uint64_t* bar = reinterpret_cast<uint64_t*>(red + 16);
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 1);
+  static_assert(512 + (256 + 128 + 3 * 512 + 16) * 4 + 16 <= kGradScal, "the scalars fit");
 
   grid_dependency_wait();
   allow_dependent_launch();
@@ -113,9 +115,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
     tc_fence_after();
   };
 
-  float acc[kHalf];  // dQ or dK of this row
+  float acc[kCols];  // dQ or dK of this row
 #pragma unroll
-  for (int i = 0; i < kHalf; ++i) acc[i] = 0.f;
+  for (int i = 0; i < kCols; ++i) acc[i] = 0.f;
 
   const int group = a.Hv / a.Hk;
   for (int r = 0; r < group; ++r) {
@@ -123,9 +125,14 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
     const long long hs = slot * a.Hv + h;
     const float4* S4 = reinterpret_cast<const float4*>(a.s_ws + hs * KD * VD * 4);
     const float4* D4 = reinterpret_cast<const float4*>(a.d_ws + hs * KD * VD * 4);
-    float4 sv[kF4];
+    // two neighbouring column tiles of a strip per warp and step
+    auto pair_off = [&](int i) { return ((warp + i * (kGradThreads / 32)) * 2) * 32 + lane; };
+    float4 sv[2 * kPair];
 #pragma unroll
-    for (int i = 0; i < kF4; ++i) sv[i] = S4[tid + i * kGradThreads];
+    for (int i = 0; i < kPair; ++i) {
+      sv[2 * i] = S4[pair_off(i)];
+      sv[2 * i + 1] = S4[pair_off(i) + 32];
+    }
 #pragma unroll
     for (int vt = 0; vt < kVT; ++vt) {
       const uint32_t at = aA + vt * 5 * kTileBytes;
@@ -148,13 +155,13 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
         const double o = __shfl_up_sync(0xffffffffu, s, off);
         if (lane >= off) s += o;
       }
-      Gs[ta] = s - static_cast<double>(gb);
-      Gs[tb] = s;
+      Gs[ta] = decay_sum(s - static_cast<double>(gb));
+      Gs[tb] = decay_sum(s);
     } else {
       const float* ps = reinterpret_cast<const float*>(a.prep + hs * kPrepBytes + kPrepTri);
       for (int i = tid - 32; i < 193; i += kGradThreads - 32) scal[i] = ps[i];
       // the strips' shares of b and dbeta, in strip order
-      if (tid >= 128) {
+      if (tid >= 128 && tid < 256) {
         const int which = (tid - 128) >> 6, t = tid & 63;
         const float* p = a.dots + hs * (VD / 16) * 128 + which * 64 + t;
         float v = 0.f;
@@ -163,21 +170,21 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
         (which == 0 ? bsum : dbs)[t] = v;
       }
     }
-    // a state in fragment order -> hi and lo tiles [v][k]
+    // a state in fragment order -> hi and lo tiles [v][k], four 8 x 8 matrices a step
     auto state_tiles = [&](const float4* x) {
 #pragma unroll
-      for (int i = 0; i < kF4; ++i) {
-        const int f = tid + i * kGradThreads;
-        const int ln = f & 31, n = (f >> 5) % (KD / 8), strip = (f >> 5) / (KD / 8);
-        const int v = strip * 16 + (ln >> 2);
-        uint8_t* dst = smem + L::kBig + ((v >> 6) * kKT + (n >> 3)) * kTileBytes + (ln & 3) * 4;
-        uint32_t hi, lo;
-        split2(x[i].x, x[i].y, hi, lo);
-        *reinterpret_cast<uint32_t*>(dst + tile_off(v & 63, n & 7)) = hi;
-        *reinterpret_cast<uint32_t*>(dst + L::kState / 2 + tile_off(v & 63, n & 7)) = lo;
-        split2(x[i].z, x[i].w, hi, lo);
-        *reinterpret_cast<uint32_t*>(dst + tile_off((v & 63) + 8, n & 7)) = hi;
-        *reinterpret_cast<uint32_t*>(dst + L::kState / 2 + tile_off((v & 63) + 8, n & 7)) = lo;
+      for (int i = 0; i < kPair; ++i) {
+        const int pr = warp + i * (kGradThreads / 32);
+        const int n = (pr % (KD / 16)) * 2 + (lane >> 4);  // this lane's row of a matrix
+        const int v = (pr / (KD / 16)) * 16 + (lane & 15);
+        const uint32_t dst = big + ((v >> 6) * kKT + (n >> 3)) * kTileBytes + tile_off(v & 63, n & 7);
+        uint32_t hi[4], lo[4];
+        split2(x[2 * i].x, x[2 * i].y, hi[0], lo[0]);
+        split2(x[2 * i].z, x[2 * i].w, hi[1], lo[1]);
+        split2(x[2 * i + 1].x, x[2 * i + 1].y, hi[2], lo[2]);
+        split2(x[2 * i + 1].z, x[2 * i + 1].w, hi[3], lo[3]);
+        stsm4(dst, hi);
+        stsm4(dst + L::kState / 2, lo);
       }
     };
     state_tiles(sv);
@@ -214,29 +221,32 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
       tc_commit(bar);
     }
     // meanwhile D, and <S, D>
-    float4 dv4[kF4];
+    float4 dd[2 * kPair];
 #pragma unroll
-    for (int i = 0; i < kF4; ++i) dv4[i] = D4[tid + i * kGradThreads];
+    for (int i = 0; i < kPair; ++i) {
+      dd[2 * i] = D4[pair_off(i)];
+      dd[2 * i + 1] = D4[pair_off(i) + 32];
+    }
     {
       float v = 0.f;
 #pragma unroll
-      for (int i = 0; i < kF4; ++i)
-        v += sv[i].x * dv4[i].x + sv[i].y * dv4[i].y + sv[i].z * dv4[i].z + sv[i].w * dv4[i].w;
+      for (int i = 0; i < 2 * kPair; ++i)
+        v += sv[i].x * dd[i].x + sv[i].y * dd[i].y + sv[i].z * dd[i].z + sv[i].w * dd[i].w;
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
       if (lane == 0) red[warp] = v;
     }
     wait_mma();
     // ---- D takes S's place
-    state_tiles(dv4);
+    state_tiles(dd);
     // E (key side) or F, and the second part of E before its range is used again
-    float ef[32];
-    tc_load32(mine + kD2 + half * 32, ef);
+    float ef[16];
+    tc_load16(mine + kD2 + cq * 16, ef);
     if (key_side) {
-      float t[32];
-      tc_load32(mine + kD2b + half * 32, t);
+      float t[16];
+      tc_load16(mine + kD2b + cq * 16, t);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) ef[i] += t[i];
+      for (int i = 0; i < 16; ++i) ef[i] += t[i];
     }
     fence_smem_to_async();
     tc_fence_before();
@@ -263,19 +273,19 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
       const float f = key_side ? -scal[64 + tok] : a.scale * scal[64 + tok];
       float dot = 0.f;
 #pragma unroll
-      for (int c = 0; c < kHalf / 32; ++c) {
-        float t[32];
-        tc_load32(mine + kD1 + half * kHalf + c * 32, t);
+      for (int c = 0; c < kCols / 16; ++c) {
+        float t[16];
+        tc_load16(mine + kD1 + cq * kCols + c * 16, t);
         if (key_side) {
-          float u[32];
-          tc_load32(mine + kD1b + half * kHalf + c * 32, u);
+          float u[16];
+          tc_load16(mine + kD1b + cq * kCols + c * 16, u);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) t[i] += u[i];
+          for (int i = 0; i < 16; ++i) t[i] += u[i];
         }
-        const int col = half * kHalf + c * 32;
+        const int col = cq * kCols + c * 16;
         const uint8_t* src = smem + L::kQK + ((col >> 6) * 2 + (key_side ? 1 : 0)) * kTileBytes;
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
+        for (int p = 0; p < 2; ++p) {
           const uint4 x = *reinterpret_cast<const uint4*>(src + tile_off(tok, ((col & 63) >> 3) + p));
           float xf[8];
           bf16x8_to_f32(x, xf);
@@ -283,30 +293,29 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
           for (int e = 0; e < 8; ++e) {
             const float v = f * t[p * 8 + e];
             dot = fmaf(v, xf[e], dot);
-            acc[c * 32 + p * 8 + e] += v;
+            acc[c * 16 + p * 8 + e] += v;
           }
         }
       }
-      adot[(half * 2 + (key_side ? 1 : 0)) * 64 + tok] = dot;
+      adot[(cq * 2 + (key_side ? 1 : 0)) * 64 + tok] = dot;
     }
-    // ---- the pair terms: this row's 32 columns of Ph or -Eh, and of their products with q.k or k.k
-    uint32_t hi[16], lo[16];
-    {
-      float kk[32];
-      tc_load32(mine + kKK + half * 32, kk);
-      const double G = Gs[tok];
-      float run = 0.f;
+    // ---- the pair terms: this row's 16 columns of Ph or -Eh, and of their products with q.k or
+    // k.k; all zero above the diagonal
+    uint32_t hi[8], lo[8];
+    float run = 0.f;
+    if (cq * 16 <= (warp & 1) * 32 + 31) {
+      float kk[16];
+      tc_load16(mine + kKK + cq * 16, kk);
+      const float2 G = Gs[tok];
 #pragma unroll
-      for (int i = 0; i < 32; i += 2) {
+      for (int i = 0; i < 16; i += 2) {
         float p[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int j = half * 32 + i + e;
+          const int j = cq * 16 + i + e;
           float v = 0.f;
-          if (key_side ? j < tok : j <= tok) {
-            const float d = expf(static_cast<float>(G - Gs[j])) * scal[j];
-            v = key_side ? -ef[i + e] * d : a.scale * ef[i + e] * d;
-          }
+          if (key_side ? j < tok : j <= tok)
+            v = (key_side ? -ef[i + e] : a.scale * ef[i + e]) * (decay_between(G, Gs[j]) * scal[j]);
           p[e] = v;
           // running sums over the columns before, in the place of the terms
           const float m = j < tok ? v * kk[i + e] : 0.f;
@@ -315,21 +324,26 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
         }
         split2(p[0], p[1], hi[i / 2], lo[i / 2]);
       }
-      if (half == 0) rowsum[row] = run;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) hi[i] = lo[i] = 0u;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) ef[i] = 0.f;
     }
+    rowsum[cq * 128 + row] = run;
     wait_mma();  // W D^T is done, its tiles' place is free
     {
       uint8_t* dst = smem + L::kBig + (key_side ? kTileBytes : 0);
 #pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        const uint32_t off = tile_off(tok, half * 4 + p);
+      for (int p = 0; p < 2; ++p) {
+        const uint32_t off = tile_off(tok, cq * 2 + p);
         *reinterpret_cast<uint4*>(dst + off) = make_uint4(hi[4 * p], hi[4 * p + 1], hi[4 * p + 2], hi[4 * p + 3]);
         *reinterpret_cast<uint4*>(dst + 2 * kTileBytes + off) =
             make_uint4(lo[4 * p], lo[4 * p + 1], lo[4 * p + 2], lo[4 * p + 3]);
       }
-      float* M = reinterpret_cast<float*>(smem + L::kBig + 4 * kTileBytes) + row * kMLd + half * 32;
+      float* M = reinterpret_cast<float*>(smem + L::kBig + 4 * kTileBytes) + row * kMLd + cq * 16;
 #pragma unroll
-      for (int i = 0; i < 32; ++i) M[i] = ef[i];
+      for (int i = 0; i < 16; ++i) M[i] = ef[i];
     }
     fence_smem_to_async();
     tc_fence_before();
@@ -356,59 +370,82 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
     if (key_side) {
       const float f = scal[128 + tok] * scal[tok];
 #pragma unroll
-      for (int c = 0; c < kHalf / 32; ++c) {
-        float t[32];
-        tc_load32(mine + kD3 + half * kHalf + c * 32, t);
+      for (int c = 0; c < kCols / 16; ++c) {
+        float t[16];
+        tc_load16(mine + kD3 + cq * kCols + c * 16, t);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) acc[c * 32 + i] = fmaf(f, t[i], acc[c * 32 + i]);
+        for (int i = 0; i < 16; ++i) acc[c * 16 + i] = fmaf(f, t[i], acc[c * 16 + i]);
       }
     }
     {
-      // column t of the running sums: rows i >= t of 32 rows of Ph's or Eh's terms
+      // column t of the running sums: rows i >= t of 16 rows of Ph's or Eh's terms
       const int t = tid & 63, part = tid >> 6;
-      const int i0 = (part & 1) * 32, r0 = (part >> 1) * 64 + i0;
+      const int i0 = (part & 3) * 16, r0 = (part >> 2) * 64 + i0;
       const float* M = reinterpret_cast<const float*>(smem + L::kBig + 4 * kTileBytes) + r0 * kMLd + t;
       float v = 0.f;
-#pragma unroll 8
-      for (int i = 0; i < 32; ++i) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
         float x = M[i * kMLd];
-        if (t >= 32) x += rowsum[r0 + i];  // the second half's sums start at the first half's
+        // the sums of a quarter start at those of the quarters before
+        for (int c = 0; c < (t >> 4); ++c) x += rowsum[c * 128 + r0 + i];
         v += i0 + i >= t ? x : 0.f;
       }
       vpart[part * 64 + t] = v;
     }
     __syncthreads();
-    if (tid < 64) {
-      float v = vpart[tid] + vpart[64 + tid] + vpart[128 + tid] + vpart[192 + tid];
-      float pa = 0.f, pb = 0.f, sd = 0.f;
+    if (warp == 0) {
+      // two tokens a lane: sums of a over i >= t and of b over j < t
+      float sd = 0.f, sa[2], pb[2], v[2] = {0.f, 0.f};
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sd += red[i];
-#pragma unroll 8
-      for (int i = 0; i < 64; ++i) {
-        pa += i >= tid ? (adot[i] + adot[64 + i]) + (adot[128 + i] + adot[192 + i]) : 0.f;
-        pb += i < tid ? bsum[i] : 0.f;
+      for (int i = 0; i < kGradThreads / 32; ++i) sd += red[i];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int t = lane + 32 * u;
+        sa[u] = 0.f;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          sa[u] += adot[c * 64 + t];
+          v[u] += vpart[c * 64 + t];
+        }
+        const float bt = bsum[t];
+        pb[u] = bt;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+          const float x = __shfl_down_sync(0xffffffffu, sa[u], off);
+          const float y = __shfl_up_sync(0xffffffffu, pb[u], off);
+          if (lane + off < 32) sa[u] += x;
+          if (lane >= off) pb[u] += y;
+        }
       }
-      if (tid < live) {
-        const long long t = t0 + tid;
-        a.dg[t * a.lddg + h] = scal[192] * sd + v + pa + pb;
-        const float db = dbs[tid];
-        if (a.beta_fp32)
-          reinterpret_cast<float*>(a.dbeta)[t * a.lddbeta + h] = db;
-        else
-          reinterpret_cast<__nv_bfloat16*>(a.dbeta)[t * a.lddbeta + h] = __float2bfloat16_rn(db);
+      sa[0] += __shfl_sync(0xffffffffu, sa[1], 0);
+      const float first = __shfl_sync(0xffffffffu, pb[0], 31);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const float incl = __shfl_up_sync(0xffffffffu, pb[u], 1);
+        const float before = (lane > 0 ? incl : 0.f) + (u > 0 ? first : 0.f);
+        const int tk = lane + 32 * u;
+        if (tk < live) {
+          const long long t = t0 + tk;
+          a.dg[t * a.lddg + h] = scal[192] * sd + v[u] + sa[u] + before;
+          const float db = dbs[tk];
+          if (a.beta_fp32)
+            reinterpret_cast<float*>(a.dbeta)[t * a.lddbeta + h] = db;
+          else
+            reinterpret_cast<__nv_bfloat16*>(a.dbeta)[t * a.lddbeta + h] = __float2bfloat16_rn(db);
+        }
       }
     }
     wait_mma();
 #pragma unroll
-    for (int c = 0; c < kHalf / 32; ++c) {
-      float t[32];
-      tc_load32(mine + kD4 + half * kHalf + c * 32, t);
+    for (int c = 0; c < kCols / 16; ++c) {
+      float t[16];
+      tc_load16(mine + kD4 + cq * kCols + c * 16, t);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) acc[c * 32 + i] += t[i];
+      for (int i = 0; i < 16; ++i) acc[c * 16 + i] += t[i];
       if (key_side) {
-        tc_load32(mine + kD5 + half * kHalf + c * 32, t);
+        tc_load16(mine + kD5 + cq * kCols + c * 16, t);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) acc[c * 32 + i] += t[i];
+        for (int i = 0; i < 16; ++i) acc[c * 16 + i] += t[i];
       }
     }
     tc_fence_before();
@@ -416,9 +453,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
   }
   if (tok < live) {
     uint16_t* dst = key_side ? a.dk + (t0 + tok) * a.lddk : a.dq + (t0 + tok) * a.lddq;
-    dst += static_cast<long long>(hk) * KD + half * kHalf;
+    dst += static_cast<long long>(hk) * KD + cq * kCols;
 #pragma unroll
-    for (int i = 0; i < kHalf / 8; ++i)
+    for (int i = 0; i < kCols / 8; ++i)
       *reinterpret_cast<uint4*>(dst + i * 8) = f32x8_to_bf16(acc + i * 8);
   }
   if (warp == 0) tmem_free(tmem, 512);
