@@ -60,8 +60,9 @@ cudaError_t launch_scan_bwd(const DeltaArgs& a, cudaStream_t s) {
 }
 
 template <int KD, int VD>
-cudaError_t launch_grad(const DeltaArgs& a, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>(delta_slots(a.seq.T, a.seq.B)), static_cast<unsigned>(a.Hk));
+cudaError_t launch_grad(const DeltaArgs& a, int num_sms, cudaStream_t s) {
+  const long long units = a.slots * a.Hk;
+  const dim3 grid(static_cast<unsigned>(units < num_sms ? units : num_sms));
   return launch_grid(delta_grad_kernel<KD, VD>, grid, kGradThreads, GradSmem<KD, VD>::kBytes, s, a);
 }
 
@@ -81,7 +82,7 @@ cudaError_t run_bwd(const DeltaArgs& a, int num_sms, cudaStream_t s) {
                                    : launch_scan_fwd<KD, 2, false, true>(a, s);
   if (e == cudaSuccess) e = launch_scan_bwd<KD>(a, s);
   if (e == cudaSuccess)
-    e = a.V == 64 ? launch_grad<KD, 64>(a, s) : launch_grad<KD, 128>(a, s);
+    e = a.V == 64 ? launch_grad<KD, 64>(a, num_sms, s) : launch_grad<KD, 128>(a, num_sms, s);
   return e;
 }
 
@@ -317,6 +318,7 @@ int gnorm_delta_bwd(const gnorm_delta_bwd_desc* desc, void* stream) {
   DeviceInfo info;
   if ((st = device_info(&info)) != GNORM_OK) return st;
   a.err = info.err_word;
+  a.slots = delta_slots(d.T, d.B);
   const cudaStream_t s = as_stream(stream);
   const cudaError_t e =
       d.K == 64 ? run_bwd<64>(a, info.num_sms, s) : run_bwd<128>(a, info.num_sms, s);

@@ -14,7 +14,7 @@
 //   dg_t = e^{G_C} <S, D> + sum_{i>=t} a_i + sum_{j<t} b_j + sum_{i>=t>j} (Ph_ij q_i.k_j - Eh_ij k_i.k_j)
 //   a_i = scale gamma_i (q_i S).dO_i - gamma_i (k_i S).dX_i      b_j = lambda_j beta_j (k_j D).W_j
 //
-// One CTA per (chunk, key head) goes through the value heads of the group and adds their dQ
+// A CTA takes a chunk and key head, goes through the value heads of the group and adds their dQ
 // and dK in registers, so the sum over shared heads has a fixed order.
 //
 // Everything here is products of 64-token tiles, done by tcgen05.  An instruction has 128
@@ -24,6 +24,11 @@
 // (W D^T, the transposed Ph and Eh, the second parts of dX and W) the upper rows multiply
 // whatever tile lies before it and are not read.  A thread owns one row and a quarter of the columns.
 // Operands that are not exact in BF16 are in two parts here: dq and dk are BF16.
+//
+// The products of a chunk and head take about 5600 cycles of the tensor cores, what it reads
+// (S and D in FP32, W, dX, dO: 240 KB) as long again.  A CTA stays on its SM and goes through
+// its chunks; the next one's tiles are copied, its S loaded and its scalars computed behind
+// the products of the current one.
 #pragma once
 
 #include "delta_common.cuh"
@@ -34,19 +39,30 @@ namespace gnorm {
 constexpr int kGradThreads = 512;
 constexpr int kMLd = 65;
 constexpr unsigned kErrWaitMma = 8u;  // a wait for the tensor cores ran out
-constexpr int kGradScal = 9216;
 
 template <int KD, int VD>
 struct GradSmem {
-  // [q][k] of each 64 columns of K, then [do][dX hi][dX lo][W hi][W lo] of each 64 columns of V
+  // [q][k] of each 64 columns of K, twice; then [do][dX hi][dX lo][W hi][W lo] of each 64
+  // columns of V
   static constexpr int kQK = 0;
-  static constexpr int kA = kQK + KD / 64 * 2 * kTileBytes;
-  // S, then D (hi and lo tiles); then Ph, -Eh (hi, then lo) and the pair terms' running sums
+  static constexpr int kQKBytes = KD / 64 * 2 * kTileBytes;
+  static constexpr int kA = 2 * kQKBytes;
+  // S, then D (hi and lo tiles); then Ph, -Eh (hi, then lo) and the pair terms' running sums;
+  // then dq and dk on their way out
   static constexpr int kBig = kA + VD / 64 * 5 * kTileBytes;
   static constexpr int kState = 2 * (VD / 64) * (KD / 64) * kTileBytes;
   static constexpr int kPairs = 4 * kTileBytes + 128 * kMLd * 4;
   static constexpr int kScal = kBig + (kState > kPairs ? kState : kPairs);
-  static constexpr int kBytes = kScal + kGradScal + 1024;  // 1024: the tiles' alignment
+  // per item, twice: decay sums [64], beta, gamma, lambda, e^{G_C}, b and dbeta sums
+  static constexpr int kItem = 512 + 1024 + 512;
+  static constexpr int kWork = kScal + 2 * kItem;  // sums within an item
+  static constexpr int kBytes = kWork + (3 * 512 + 16) * 4 + 16 + 1024;  // 1024: alignment
+};
+
+// What a CTA works on: a chunk and key head with live tokens, and one of its value heads.
+struct GradItem {
+  long long unit, slot, t0;
+  int hk, r, live;
 };
 
 template <int KD, int VD>
@@ -66,41 +82,121 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
   const int cq = warp >> 2;                             // quarter of the columns
   const bool key_side = (warp & 2) != 0;
   const int tok = row & 63;
-  const long long slot = blockIdx.x;
-  const int hk = blockIdx.y;
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t s0 = smem_u32(smem);
-  float2* Gs = reinterpret_cast<float2*>(smem + L::kScal);          // [64]
-  float* scal = reinterpret_cast<float*>(smem + L::kScal + 512);    // beta, gamma, lambda, e^{G_C}
-  float* bsum = scal + 256;                                         // [64]
-  float* dbs = bsum + 64;                                           // [64]
-  float* adot = dbs + 64;                                           // [8][64]
+  float* adot = reinterpret_cast<float*>(smem + L::kWork);          // [8][64]
   float* vpart = adot + 512;                                        // [8][64]
   float* rowsum = vpart + 512;                                      // [4][128]
   float* red = rowsum + 512;                                        // [16]
   uint64_t* bar = reinterpret_cast<uint64_t*>(red + 16);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 1);
-  static_assert(512 + (256 + 128 + 3 * 512 + 16) * 4 + 16 <= kGradScal, "the scalars fit");
 
   grid_dependency_wait();
   allow_dependent_launch();
-  const int b = seq_of_slot(a.seq, slot, lane);
-  const long long chunk = slot - seq_base(a.seq, b);
-  const long long t0 = seq_start(a.seq, b) + chunk * kChunk;
-  const long long left = seq_end(a.seq, b) - t0;
-  if (b == a.seq.B || chunk < 0 || left <= 0) return;
-  const int live = static_cast<int>(left < kChunk ? left : kChunk);
+  const int group = a.Hv / a.Hk;
+  const long long units = a.slots * a.Hk;
+  // the first unit from u on (in this CTA's steps) that has tokens
+  auto find = [&](long long u) {
+    GradItem it{};
+    for (; u < units; u += gridDim.x) {
+      it.slot = u / a.Hk;
+      const int b = seq_of_slot(a.seq, it.slot, lane);
+      const long long chunk = it.slot - seq_base(a.seq, b);
+      it.t0 = seq_start(a.seq, b) + chunk * kChunk;
+      const long long left = seq_end(a.seq, b) - it.t0;
+      if (b == a.seq.B || chunk < 0 || left <= 0) continue;
+      it.hk = static_cast<int>(u - it.slot * a.Hk);
+      it.live = static_cast<int>(left < kChunk ? left : kChunk);
+      break;
+    }
+    it.unit = u;
+    return it;
+  };
+  auto next_item = [&](const GradItem& c) {
+    if (c.r + 1 == group) return find(c.unit + gridDim.x);
+    GradItem it = c;
+    ++it.r;
+    return it;
+  };
+  GradItem cur = find(blockIdx.x);
+  if (cur.unit >= units) return;
+
+  // two neighbouring column tiles of a strip per warp and step
+  auto pair_off = [&](int i) { return ((warp + i * (kGradThreads / 32)) * 2) * 32 + lane; };
+  float4 sv[2 * kPair];
+  auto load_s = [&](const GradItem& it) {
+    const long long hs = it.slot * a.Hv + it.hk * group + it.r;
+    const float4* S4 = reinterpret_cast<const float4*>(a.s_ws + hs * KD * VD * 4);
+#pragma unroll
+    for (int i = 0; i < kPair; ++i) {
+      sv[2 * i] = S4[pair_off(i)];
+      sv[2 * i + 1] = S4[pair_off(i) + 32];
+    }
+  };
+  auto load_tiles = [&](const GradItem& it, int qk_buf) {
+    const int h = it.hk * group + it.r;
+    const long long hs = it.slot * a.Hv + h;
+    if (it.r == 0) {
+#pragma unroll
+      for (int kt = 0; kt < kKT; ++kt) {
+        const long long col = static_cast<long long>(it.hk) * KD + kt * 64;
+        const uint32_t at = s0 + L::kQK + qk_buf * L::kQKBytes + kt * 2 * kTileBytes;
+        load_rows<kGradThreads>(at, a.q + it.t0 * a.ldq + col, a.ldq, 64, it.live, tid);
+        load_rows<kGradThreads>(at + kTileBytes, a.k + it.t0 * a.ldk + col, a.ldk, 64, it.live, tid);
+      }
+    }
+#pragma unroll
+    for (int vt = 0; vt < kVT; ++vt) {
+      const uint32_t at = s0 + L::kA + vt * 5 * kTileBytes;
+      const long long col = static_cast<long long>(h) * VD + vt * 64;
+      load_rows<kGradThreads>(at, a.dout + it.t0 * a.lddo + col, a.lddo, 64, it.live, tid);
+      load_rows<kGradThreads>(at + kTileBytes, a.dv + it.t0 * a.lddv + col, a.lddv, 64, it.live, tid);
+      load_flat<kGradThreads>(at + 2 * kTileBytes, a.x_ws + (hs * kVT + vt) * kTileBytes, kTileBytes, tid);
+      const uint8_t* w = a.w_ws + (hs * 3 * kVT + vt) * kTileBytes;
+      load_flat<kGradThreads>(at + 3 * kTileBytes, w, kTileBytes, tid);
+      load_flat<kGradThreads>(at + 4 * kTileBytes, w + kVT * kTileBytes, kTileBytes, tid);
+    }
+    cp_commit();
+  };
+  auto item_scalars = [&](int buf) { return smem + L::kScal + buf * L::kItem; };
+  auto load_scalars = [&](const GradItem& it, int buf) {
+    const int h = it.hk * group + it.r;
+    const long long hs = it.slot * a.Hv + h;
+    float2* Gs = reinterpret_cast<float2*>(item_scalars(buf));
+    float* scal = reinterpret_cast<float*>(item_scalars(buf) + 512);
+    if (warp == 0) {
+      const int ta = 2 * lane, tb = ta + 1;
+      const float ga = ta < it.live ? clamp_decay(a.g[(it.t0 + ta) * a.ldg + h]) : 0.f;
+      const float gb = tb < it.live ? clamp_decay(a.g[(it.t0 + tb) * a.ldg + h]) : 0.f;
+      double s = static_cast<double>(ga) + static_cast<double>(gb);
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const double o = __shfl_up_sync(0xffffffffu, s, off);
+        if (lane >= off) s += o;
+      }
+      Gs[ta] = decay_sum(s - static_cast<double>(gb));
+      Gs[tb] = decay_sum(s);
+    } else if (tid < 256) {
+      const float* ps = reinterpret_cast<const float*>(a.prep + hs * kPrepBytes + kPrepTri);
+      if (tid - 32 < 193) scal[tid - 32] = ps[tid - 32];
+    } else if (tid < 384) {
+      // the strips' shares of b and dbeta, in strip order
+      const float* p = a.dots + hs * (VD / 16) * 128 + (tid - 256);
+      float v = 0.f;
+#pragma unroll
+      for (int i = 0; i < VD / 16; ++i) v += p[i * 128];
+      scal[tid] = v;  // [256..319] b, [320..383] dbeta
+    }
+  };
+
+  load_tiles(cur, 0);
+  load_s(cur);
   if (warp == 0) tmem_alloc(tslot, 512);
   if (tid == 32) {
     mbar_init(bar, 1);
     fence_barrier_init();
   }
-#pragma unroll
-  for (int kt = 0; kt < kKT; ++kt) {
-    const long long col = static_cast<long long>(hk) * KD + kt * 64;
-    load_rows<kGradThreads>(s0 + L::kQK + kt * 2 * kTileBytes, a.q + t0 * a.ldq + col, a.ldq, 64, live, tid);
-    load_rows<kGradThreads>(s0 + L::kQK + (kt * 2 + 1) * kTileBytes, a.k + t0 * a.ldk + col, a.ldk, 64, live, tid);
-  }
+  load_scalars(cur, 0);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -114,79 +210,36 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
     phase ^= 1u;
     tc_fence_after();
   };
-
-  float acc[kCols];  // dQ or dK of this row
-#pragma unroll
-  for (int i = 0; i < kCols; ++i) acc[i] = 0.f;
-
-  const int group = a.Hv / a.Hk;
-  for (int r = 0; r < group; ++r) {
-    const int h = hk * group + r;
-    const long long hs = slot * a.Hv + h;
-    const float4* S4 = reinterpret_cast<const float4*>(a.s_ws + hs * KD * VD * 4);
-    const float4* D4 = reinterpret_cast<const float4*>(a.d_ws + hs * KD * VD * 4);
-    // two neighbouring column tiles of a strip per warp and step
-    auto pair_off = [&](int i) { return ((warp + i * (kGradThreads / 32)) * 2) * 32 + lane; };
-    float4 sv[2 * kPair];
+  // a state in fragment order -> hi and lo tiles [v][k], four 8 x 8 matrices a step
+  auto state_tiles = [&](const float4* x) {
 #pragma unroll
     for (int i = 0; i < kPair; ++i) {
-      sv[2 * i] = S4[pair_off(i)];
-      sv[2 * i + 1] = S4[pair_off(i) + 32];
+      const int pr = warp + i * (kGradThreads / 32);
+      const int n = (pr % (KD / 16)) * 2 + (lane >> 4);  // this lane's row of a matrix
+      const int v = (pr / (KD / 16)) * 16 + (lane & 15);
+      const uint32_t dst = big + ((v >> 6) * kKT + (n >> 3)) * kTileBytes + tile_off(v & 63, n & 7);
+      uint32_t hi[4], lo[4];
+      split2(x[2 * i].x, x[2 * i].y, hi[0], lo[0]);
+      split2(x[2 * i].z, x[2 * i].w, hi[1], lo[1]);
+      split2(x[2 * i + 1].x, x[2 * i + 1].y, hi[2], lo[2]);
+      split2(x[2 * i + 1].z, x[2 * i + 1].w, hi[3], lo[3]);
+      stsm4(dst, hi);
+      stsm4(dst + L::kState / 2, lo);
     }
+  };
+
+  float acc[kCols];  // dQ or dK of this row
+  int buf = 0, qk_buf = 0;
+  while (true) {
+    const int h = cur.hk * group + cur.r;
+    const long long hs = cur.slot * a.Hv + h;
+    const float2* Gs = reinterpret_cast<const float2*>(item_scalars(buf));
+    const float* scal = reinterpret_cast<const float*>(item_scalars(buf) + 512);
+    const uint32_t qk = s0 + L::kQK + qk_buf * L::kQKBytes;
+    if (cur.r == 0) {
 #pragma unroll
-    for (int vt = 0; vt < kVT; ++vt) {
-      const uint32_t at = aA + vt * 5 * kTileBytes;
-      const long long col = static_cast<long long>(h) * VD + vt * 64;
-      load_rows<kGradThreads>(at, a.dout + t0 * a.lddo + col, a.lddo, 64, live, tid);
-      load_rows<kGradThreads>(at + kTileBytes, a.dv + t0 * a.lddv + col, a.lddv, 64, live, tid);
-      load_flat<kGradThreads>(at + 2 * kTileBytes, a.x_ws + (hs * kVT + vt) * kTileBytes, kTileBytes, tid);
-      const uint8_t* w = a.w_ws + (hs * 3 * kVT + vt) * kTileBytes;
-      load_flat<kGradThreads>(at + 3 * kTileBytes, w, kTileBytes, tid);
-      load_flat<kGradThreads>(at + 4 * kTileBytes, w + kVT * kTileBytes, kTileBytes, tid);
+      for (int i = 0; i < kCols; ++i) acc[i] = 0.f;
     }
-    cp_commit();
-    if (warp == 0) {
-      const int ta = 2 * lane, tb = ta + 1;
-      const float ga = ta < live ? clamp_decay(a.g[(t0 + ta) * a.ldg + h]) : 0.f;
-      const float gb = tb < live ? clamp_decay(a.g[(t0 + tb) * a.ldg + h]) : 0.f;
-      double s = static_cast<double>(ga) + static_cast<double>(gb);
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const double o = __shfl_up_sync(0xffffffffu, s, off);
-        if (lane >= off) s += o;
-      }
-      Gs[ta] = decay_sum(s - static_cast<double>(gb));
-      Gs[tb] = decay_sum(s);
-    } else {
-      const float* ps = reinterpret_cast<const float*>(a.prep + hs * kPrepBytes + kPrepTri);
-      for (int i = tid - 32; i < 193; i += kGradThreads - 32) scal[i] = ps[i];
-      // the strips' shares of b and dbeta, in strip order
-      if (tid >= 128 && tid < 256) {
-        const int which = (tid - 128) >> 6, t = tid & 63;
-        const float* p = a.dots + hs * (VD / 16) * 128 + which * 64 + t;
-        float v = 0.f;
-#pragma unroll
-        for (int i = 0; i < VD / 16; ++i) v += p[i * 128];
-        (which == 0 ? bsum : dbs)[t] = v;
-      }
-    }
-    // a state in fragment order -> hi and lo tiles [v][k], four 8 x 8 matrices a step
-    auto state_tiles = [&](const float4* x) {
-#pragma unroll
-      for (int i = 0; i < kPair; ++i) {
-        const int pr = warp + i * (kGradThreads / 32);
-        const int n = (pr % (KD / 16)) * 2 + (lane >> 4);  // this lane's row of a matrix
-        const int v = (pr / (KD / 16)) * 16 + (lane & 15);
-        const uint32_t dst = big + ((v >> 6) * kKT + (n >> 3)) * kTileBytes + tile_off(v & 63, n & 7);
-        uint32_t hi[4], lo[4];
-        split2(x[2 * i].x, x[2 * i].y, hi[0], lo[0]);
-        split2(x[2 * i].z, x[2 * i].w, hi[1], lo[1]);
-        split2(x[2 * i + 1].x, x[2 * i + 1].y, hi[2], lo[2]);
-        split2(x[2 * i + 1].z, x[2 * i + 1].w, hi[3], lo[3]);
-        stsm4(dst, hi);
-        stsm4(dst + L::kState / 2, lo);
-      }
-    };
     state_tiles(sv);
     cp_wait<0>();
     fence_smem_to_async();
@@ -211,22 +264,28 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
         tc_mma(tmem + kD2, a0, wl, idW, true);
         tc_mma(tmem + kD2b, a1, wh, idW, ks > 0);
       }
-      if (r == 0) {
+      if (cur.r == 0) {
 #pragma unroll
         for (int ks = 0; ks < KD / 16; ++ks) {
-          const uint32_t at = s0 + L::kQK + (ks >> 2) * 2 * kTileBytes + (ks & 3) * 32;
+          const uint32_t at = qk + (ks >> 2) * 2 * kTileBytes + (ks & 3) * 32;
           tc_mma(tmem + kKK, smem_desc(at, 16, 1024), smem_desc(at + kTileBytes, 16, 1024), idW, ks > 0);
         }
       }
       tc_commit(bar);
     }
-    // meanwhile D, and <S, D>
+    // meanwhile D, the next item with its scalars, and <S, D>
     float4 dd[2 * kPair];
+    {
+      const float4* D4 = reinterpret_cast<const float4*>(a.d_ws + hs * KD * VD * 4);
 #pragma unroll
-    for (int i = 0; i < kPair; ++i) {
-      dd[2 * i] = D4[pair_off(i)];
-      dd[2 * i + 1] = D4[pair_off(i) + 32];
+      for (int i = 0; i < kPair; ++i) {
+        dd[2 * i] = D4[pair_off(i)];
+        dd[2 * i + 1] = D4[pair_off(i) + 32];
+      }
     }
+    const GradItem nxt = next_item(cur);
+    const bool more = nxt.unit < units;
+    if (more) load_scalars(nxt, buf ^ 1);
     {
       float v = 0.f;
 #pragma unroll
@@ -268,37 +327,6 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
       }
       tc_commit(bar);
     }
-    // ---- meanwhile the products with S: scale the row, add, and its product with q or k (a_i)
-    {
-      const float f = key_side ? -scal[64 + tok] : a.scale * scal[64 + tok];
-      float dot = 0.f;
-#pragma unroll
-      for (int c = 0; c < kCols / 16; ++c) {
-        float t[16];
-        tc_load16(mine + kD1 + cq * kCols + c * 16, t);
-        if (key_side) {
-          float u[16];
-          tc_load16(mine + kD1b + cq * kCols + c * 16, u);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) t[i] += u[i];
-        }
-        const int col = cq * kCols + c * 16;
-        const uint8_t* src = smem + L::kQK + ((col >> 6) * 2 + (key_side ? 1 : 0)) * kTileBytes;
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          const uint4 x = *reinterpret_cast<const uint4*>(src + tile_off(tok, ((col & 63) >> 3) + p));
-          float xf[8];
-          bf16x8_to_f32(x, xf);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float v = f * t[p * 8 + e];
-            dot = fmaf(v, xf[e], dot);
-            acc[c * 16 + p * 8 + e] += v;
-          }
-        }
-      }
-      adot[(cq * 2 + (key_side ? 1 : 0)) * 64 + tok] = dot;
-    }
     // ---- the pair terms: this row's 16 columns of Ph or -Eh, and of their products with q.k or
     // k.k; all zero above the diagonal
     uint32_t hi[8], lo[8];
@@ -331,7 +359,40 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
       for (int i = 0; i < 16; ++i) ef[i] = 0.f;
     }
     rowsum[cq * 128 + row] = run;
-    wait_mma();  // W D^T is done, its tiles' place is free
+    // ---- the products with S: scale the row, add, and its product with q or k (a_i)
+    {
+      const float f = key_side ? -scal[64 + tok] : a.scale * scal[64 + tok];
+      float dot = 0.f;
+#pragma unroll
+      for (int c = 0; c < kCols / 16; ++c) {
+        float t[16];
+        tc_load16(mine + kD1 + cq * kCols + c * 16, t);
+        if (key_side) {
+          float u[16];
+          tc_load16(mine + kD1b + cq * kCols + c * 16, u);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) t[i] += u[i];
+        }
+        const int col = cq * kCols + c * 16;
+        const uint8_t* src = smem + L::kQK + qk_buf * L::kQKBytes +
+                             ((col >> 6) * 2 + (key_side ? 1 : 0)) * kTileBytes;
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          const uint4 x = *reinterpret_cast<const uint4*>(src + tile_off(tok, ((col & 63) >> 3) + p));
+          float xf[8];
+          bf16x8_to_f32(x, xf);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float v = f * t[p * 8 + e];
+            dot = fmaf(v, xf[e], dot);
+            acc[c * 16 + p * 8 + e] += v;
+          }
+        }
+      }
+      adot[(cq * 2 + (key_side ? 1 : 0)) * 64 + tok] = dot;
+    }
+    wait_mma();       // W D^T is done: its tiles' places are free
+    __syncthreads();  // and the sums of the row's other quarters are there
     {
       uint8_t* dst = smem + L::kBig + (key_side ? kTileBytes : 0);
 #pragma unroll
@@ -341,9 +402,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
         *reinterpret_cast<uint4*>(dst + 2 * kTileBytes + off) =
             make_uint4(lo[4 * p], lo[4 * p + 1], lo[4 * p + 2], lo[4 * p + 3]);
       }
+      float before = 0.f;
+      for (int c = 0; c < cq; ++c) before += rowsum[c * 128 + row];
       float* M = reinterpret_cast<float*>(smem + L::kBig + 4 * kTileBytes) + row * kMLd + cq * 16;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) M[i] = ef[i];
+      for (int i = 0; i < 16; ++i) M[i] = ef[i] + before;
     }
     fence_smem_to_async();
     tc_fence_before();
@@ -353,20 +416,24 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
       constexpr uint32_t idP = mma_desc<false, true, KD>(), idT = mma_desc<true, true, KD>();
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) {
-        const uint64_t q = smem_desc(s0 + L::kQK + ks * 2048, 2 * kTileBytes, 1024);
-        const uint64_t k = smem_desc(s0 + L::kQK + kTileBytes + ks * 2048, 2 * kTileBytes, 1024);
+        const uint64_t q = smem_desc(qk + ks * 2048, 2 * kTileBytes, 1024);
+        const uint64_t k = smem_desc(qk + kTileBytes + ks * 2048, 2 * kTileBytes, 1024);
 #pragma unroll
         for (int part = 0; part < 2; ++part) {
           const uint32_t ph = big + part * 2 * kTileBytes;
           tc_mma(tmem + kD4, smem_desc(ph + ks * 32, 16, 1024), k, idP, ks + part > 0);
-          // transposed, as rows 64..127: the tile before is rows 0..63
-          tc_mma(tmem + kD5, smem_desc(ph - kTileBytes + ks * 2048, kTileBytes, 1024), q, idT, ks + part > 0);
-          tc_mma(tmem + kD5, smem_desc(ph + ks * 2048, kTileBytes, 1024), k, idT, true);
+          // transposed, as rows 64..127 (rows 0..63, not read, are a q tile's)
+          tc_mma(tmem + kD5, smem_desc(qk + ks * 2048, ph - qk, 1024), q, idT, ks + part > 0);
+          tc_mma(tmem + kD5, smem_desc(qk + ks * 2048, ph + kTileBytes - qk, 1024), k, idT, true);
         }
       }
       tc_commit(bar);
     }
-    // ---- meanwhile W D^T, and the sums of dg over i >= t
+    // ---- meanwhile the next item's tiles and S, W D^T, and the sums of dg over i >= t
+    if (more) {
+      load_tiles(nxt, nxt.r == 0 ? qk_buf ^ 1 : qk_buf);
+      load_s(nxt);
+    }
     if (key_side) {
       const float f = scal[128 + tok] * scal[tok];
 #pragma unroll
@@ -384,12 +451,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
       const float* M = reinterpret_cast<const float*>(smem + L::kBig + 4 * kTileBytes) + r0 * kMLd + t;
       float v = 0.f;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        float x = M[i * kMLd];
-        // the sums of a quarter start at those of the quarters before
-        for (int c = 0; c < (t >> 4); ++c) x += rowsum[c * 128 + r0 + i];
-        v += i0 + i >= t ? x : 0.f;
-      }
+      for (int i = 0; i < 16; ++i) v += i0 + i >= t ? M[i * kMLd] : 0.f;
       vpart[part * 64 + t] = v;
     }
     __syncthreads();
@@ -407,8 +469,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
           sa[u] += adot[c * 64 + t];
           v[u] += vpart[c * 64 + t];
         }
-        const float bt = bsum[t];
-        pb[u] = bt;
+        pb[u] = scal[256 + t];
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
           const float x = __shfl_down_sync(0xffffffffu, sa[u], off);
@@ -424,10 +485,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
         const float incl = __shfl_up_sync(0xffffffffu, pb[u], 1);
         const float before = (lane > 0 ? incl : 0.f) + (u > 0 ? first : 0.f);
         const int tk = lane + 32 * u;
-        if (tk < live) {
-          const long long t = t0 + tk;
+        if (tk < cur.live) {
+          const long long t = cur.t0 + tk;
           a.dg[t * a.lddg + h] = scal[192] * sd + v[u] + sa[u] + before;
-          const float db = dbs[tk];
+          const float db = scal[320 + tk];
           if (a.beta_fp32)
             reinterpret_cast<float*>(a.dbeta)[t * a.lddbeta + h] = db;
           else
@@ -449,14 +510,32 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
       }
     }
     tc_fence_before();
-    __syncthreads();
-  }
-  if (tok < live) {
-    uint16_t* dst = key_side ? a.dk + (t0 + tok) * a.lddk : a.dq + (t0 + tok) * a.lddq;
-    dst += static_cast<long long>(hk) * KD + cq * kCols;
+    if (cur.r + 1 == group) {
+      // dq and dk through shared memory, so that a row leaves in whole lines
+      uint8_t* out = smem + L::kBig;
 #pragma unroll
-    for (int i = 0; i < kCols / 8; ++i)
-      *reinterpret_cast<uint4*>(dst + i * 8) = f32x8_to_bf16(acc + i * 8);
+      for (int i = 0; i < kCols / 8; ++i) {
+        const int col = cq * kCols + i * 8;
+        *reinterpret_cast<uint4*>(out + ((key_side ? kKT : 0) + (col >> 6)) * kTileBytes +
+                                  tile_off(tok, (col & 63) >> 3)) = f32x8_to_bf16(acc + i * 8);
+      }
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 2 * kKT; ++i) {
+        const int r = tid >> 3, p = tid & 7;
+        if (r < cur.live) {
+          const bool dk = i >= kKT;
+          uint16_t* dst = dk ? a.dk + (cur.t0 + r) * a.lddk : a.dq + (cur.t0 + r) * a.lddq;
+          *reinterpret_cast<uint4*>(dst + static_cast<long long>(cur.hk) * KD + (i % kKT) * 64 + p * 8) =
+              *reinterpret_cast<const uint4*>(out + i * kTileBytes + tile_off(r, p));
+        }
+      }
+    }
+    __syncthreads();
+    if (!more) break;
+    if (nxt.r == 0) qk_buf ^= 1;
+    buf ^= 1;
+    cur = nxt;
   }
   if (warp == 0) tmem_free(tmem, 512);
 }
