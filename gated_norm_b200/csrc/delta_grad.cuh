@@ -27,8 +27,8 @@
 //
 // The products of a chunk and head take about 5600 cycles of the tensor cores, what it reads
 // (S and D in FP32, W, dX, dO: 240 KB) as long again.  A CTA stays on its SM and goes through
-// its chunks; the next one's tiles are copied, its S loaded and its scalars computed behind
-// the products of the current one.
+// its chunks; the next one's tiles are copied, its states brought to L2 and its scalars computed
+// behind the products of the current one.
 #pragma once
 
 #include "delta_common.cuh"
@@ -56,7 +56,7 @@ struct GradSmem {
   // per item, twice: decay sums [64], beta, gamma, lambda, e^{G_C}, b and dbeta sums
   static constexpr int kItem = 512 + 1024 + 512;
   static constexpr int kWork = kScal + 2 * kItem;  // sums within an item
-  static constexpr int kBytes = kWork + (3 * 512 + 16) * 4 + 16 + 1024;  // 1024: alignment
+  static constexpr int kBytes = kWork + (3 * 512 + 16) * 4 + 64 + 1024;  // 1024: alignment
 };
 
 // What a CTA works on: a chunk and key head with live tokens, and one of its value heads.
@@ -64,6 +64,7 @@ struct GradItem {
   long long unit, slot, t0;
   int hk, r, live;
 };
+static_assert(sizeof(GradItem) <= 48, "the next item's place");
 
 template <int KD, int VD>
 __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __grid_constant__ DeltaArgs a) {
@@ -90,6 +91,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
   float* red = rowsum + 512;                                        // [16]
   uint64_t* bar = reinterpret_cast<uint64_t*>(red + 16);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 1);
+  GradItem* next = reinterpret_cast<GradItem*>(bar + 2);
 
   grid_dependency_wait();
   allow_dependent_launch();
@@ -123,16 +125,6 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
 
   // two neighbouring column tiles of a strip per warp and step
   auto pair_off = [&](int i) { return ((warp + i * (kGradThreads / 32)) * 2) * 32 + lane; };
-  float4 sv[2 * kPair];
-  auto load_s = [&](const GradItem& it) {
-    const long long hs = it.slot * a.Hv + it.hk * group + it.r;
-    const float4* S4 = reinterpret_cast<const float4*>(a.s_ws + hs * KD * VD * 4);
-#pragma unroll
-    for (int i = 0; i < kPair; ++i) {
-      sv[2 * i] = S4[pair_off(i)];
-      sv[2 * i + 1] = S4[pair_off(i) + 32];
-    }
-  };
   auto load_tiles = [&](const GradItem& it, int qk_buf) {
     const int h = it.hk * group + it.r;
     const long long hs = it.slot * a.Hv + h;
@@ -159,12 +151,13 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
     cp_commit();
   };
   auto item_scalars = [&](int buf) { return smem + L::kScal + buf * L::kItem; };
-  auto load_scalars = [&](const GradItem& it, int buf) {
+  // four warps, `part` 0..3
+  auto load_scalars = [&](const GradItem& it, int buf, int part) {
     const int h = it.hk * group + it.r;
     const long long hs = it.slot * a.Hv + h;
     float2* Gs = reinterpret_cast<float2*>(item_scalars(buf));
     float* scal = reinterpret_cast<float*>(item_scalars(buf) + 512);
-    if (warp == 0) {
+    if (part == 0) {
       const int ta = 2 * lane, tb = ta + 1;
       const float ga = ta < it.live ? clamp_decay(a.g[(it.t0 + ta) * a.ldg + h]) : 0.f;
       const float gb = tb < it.live ? clamp_decay(a.g[(it.t0 + tb) * a.ldg + h]) : 0.f;
@@ -176,27 +169,32 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
       }
       Gs[ta] = decay_sum(s - static_cast<double>(gb));
       Gs[tb] = decay_sum(s);
-    } else if (tid < 256) {
+    } else if (part == 1) {
       const float* ps = reinterpret_cast<const float*>(a.prep + hs * kPrepBytes + kPrepTri);
-      if (tid - 32 < 193) scal[tid - 32] = ps[tid - 32];
-    } else if (tid < 384) {
-      // the strips' shares of b and dbeta, in strip order
-      const float* p = a.dots + hs * (VD / 16) * 128 + (tid - 256);
-      float v = 0.f;
 #pragma unroll
-      for (int i = 0; i < VD / 16; ++i) v += p[i * 128];
-      scal[tid] = v;  // [256..319] b, [320..383] dbeta
+      for (int i = 0; i < 7; ++i)
+        if (lane + 32 * i < 193) scal[lane + 32 * i] = ps[lane + 32 * i];
+    } else {
+      // the strips' shares of b (part 2) and dbeta, in strip order
+      const float* p = a.dots + hs * (VD / 16) * 128 + (part - 2) * 64 + 2 * lane;
+      float2 v = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < VD / 16; ++i) {
+        const float2 x = *reinterpret_cast<const float2*>(p + i * 128);
+        v.x += x.x;
+        v.y += x.y;
+      }
+      *reinterpret_cast<float2*>(scal + 256 + (part - 2) * 64 + 2 * lane) = v;
     }
   };
 
   load_tiles(cur, 0);
-  load_s(cur);
   if (warp == 0) tmem_alloc(tslot, 512);
   if (tid == 32) {
     mbar_init(bar, 1);
     fence_barrier_init();
   }
-  load_scalars(cur, 0);
+  if (warp < 4) load_scalars(cur, 0, warp);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -206,7 +204,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
   uint32_t phase = 0;
   bool alive = true;
   auto wait_mma = [&]() {
-    if (alive) alive = mbar_wait(bar, phase, a.err, kErrWaitMma);
+    if (alive) alive = mbar_spin(bar, phase, a.err, kErrWaitMma);
     phase ^= 1u;
     tc_fence_after();
   };
@@ -239,6 +237,15 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
     if (cur.r == 0) {
 #pragma unroll
       for (int i = 0; i < kCols; ++i) acc[i] = 0.f;
+    }
+    float4 sv[2 * kPair];
+    {
+      const float4* S4 = reinterpret_cast<const float4*>(a.s_ws + hs * KD * VD * 4);
+#pragma unroll
+      for (int i = 0; i < kPair; ++i) {
+        sv[2 * i] = S4[pair_off(i)];
+        sv[2 * i + 1] = S4[pair_off(i) + 32];
+      }
     }
     state_tiles(sv);
     cp_wait<0>();
@@ -273,7 +280,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
       }
       tc_commit(bar);
     }
-    // meanwhile D, the next item with its scalars, and <S, D>
+    // meanwhile D, <S, D>, and where to go next
     float4 dd[2 * kPair];
     {
       const float4* D4 = reinterpret_cast<const float4*>(a.d_ws + hs * KD * VD * 4);
@@ -283,9 +290,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
         dd[2 * i + 1] = D4[pair_off(i) + 32];
       }
     }
-    const GradItem nxt = next_item(cur);
-    const bool more = nxt.unit < units;
-    if (more) load_scalars(nxt, buf ^ 1);
+    if (warp == kGradThreads / 32 - 1) {
+      const GradItem it = next_item(cur);
+      if (lane == 0) *next = it;
+    }
     {
       float v = 0.f;
 #pragma unroll
@@ -310,6 +318,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
     fence_smem_to_async();
     tc_fence_before();
     __syncthreads();
+    const GradItem nxt = *next;
+    const bool more = nxt.unit < units;
     if (tid == 0) {
       tc_fence_after();
       constexpr uint32_t idS = mma_desc<false, true, KD>();
@@ -357,6 +367,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
       for (int i = 0; i < 8; ++i) hi[i] = lo[i] = 0u;
 #pragma unroll
       for (int i = 0; i < 16; ++i) ef[i] = 0.f;
+      if (more) load_scalars(nxt, buf ^ 1, (warp - 8) >> 1);  // warps 8, 10, 12, 14
     }
     rowsum[cq * 128 + row] = run;
     // ---- the products with S: scale the row, add, and its product with q or k (a_i)
@@ -432,7 +443,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
     // ---- meanwhile the next item's tiles and S, W D^T, and the sums of dg over i >= t
     if (more) {
       load_tiles(nxt, nxt.r == 0 ? qk_buf ^ 1 : qk_buf);
-      load_s(nxt);
+      if (tid == 32) {  // S and D are read through registers: into L2 until then
+        const long long ns = nxt.slot * a.Hv + nxt.hk * group + nxt.r;
+        bulk_prefetch_l2(a.s_ws + ns * KD * VD * 4, KD * VD * 4);
+        bulk_prefetch_l2(a.d_ws + ns * KD * VD * 4, KD * VD * 4);
+      }
     }
     if (key_side) {
       const float f = scal[128 + tok] * scal[tok];

@@ -67,6 +67,32 @@ __device__ __forceinline__ void tc_commit(uint64_t* bar) {
                : "memory");
 }
 
+// mbar_wait for a phase that is microseconds away: polls without sleeping (a sleeping thread
+// comes back up to a microsecond late), with the same limit.
+__device__ __forceinline__ bool mbar_spin(uint64_t* bar, uint32_t parity, unsigned* err_word,
+                                          unsigned err_bit) {
+  const uint32_t addr = smem_u32(bar);
+  unsigned long long t0 = 0;
+  for (uint32_t i = 0; i < (1u << 28); ++i) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(addr), "r"(parity)
+        : "memory");
+    if (done) return true;
+    if ((i & 1023u) == 1023u) {
+      const unsigned long long t = globaltimer_ns();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > kWaitLimitNs) break;
+    }
+  }
+  atomicOr(err_word, err_bit);
+  return false;
+}
+
 // 16 columns of this warp's 32 lanes (lane = row); ready when it returns.
 __device__ __forceinline__ void tc_load16(uint32_t addr, float v[16]) {
   uint32_t r[16];
