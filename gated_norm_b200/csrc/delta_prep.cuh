@@ -5,7 +5,8 @@
 // for each value head of the group the decays, and N by forward substitution: column j of N
 // solves n_i = Kb_ij - sum_{l<i} Kb_il beta_l n_l.  Two neighbouring threads share a column,
 // each keeps half of its values in registers and reads the coefficients of row i from shared
-// memory (the same address for the whole warp), so no step waits for another warp.
+// memory (the same address for the whole warp), so no step waits for another warp.  A warp's
+// sixteen columns are zero above their diagonal block: it starts there (half of the products).
 #pragma once
 
 #include "delta_common.cuh"
@@ -30,7 +31,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(const __gri
   constexpr int kTiles = KD / 64;
   constexpr int kTileArea = prep_tile_area<KD>();
   float* kb = reinterpret_cast<float*>(smem + kTileArea);
-  double* Gs = reinterpret_cast<double*>(kb + 64 * kKbLd);
+  float2* Gs = reinterpret_cast<float2*>(kb + 64 * kKbLd);
   float* scal = reinterpret_cast<float*>(Gs + 64);  // beta, gamma, lambda [64], e^{G_C}
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const long long slot = blockIdx.x;
@@ -103,8 +104,8 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(const __gri
       }
       const double total = __shfl_sync(0xffffffffu, s, 31);
       const double Ga = s - static_cast<double>(gb);
-      Gs[ta] = Ga;
-      Gs[tb] = s;
+      Gs[ta] = decay_sum(Ga);
+      Gs[tb] = decay_sum(s);
       scal[ta] = ta < live ? load_beta(a, t0 + ta, h) : 0.f;
       scal[tb] = tb < live ? load_beta(a, t0 + tb, h) : 0.f;
       scal[64 + ta] = expf(static_cast<float>(Ga));
@@ -116,16 +117,17 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(const __gri
     __syncthreads();
     // Kb (FP32, zero on and above the diagonal) and the P tiles
     const int ra = i0 + (lane >> 2), rb = ra + 8;
-    const double Ga = Gs[ra], Gb = Gs[rb];
+    const float2 Ga = Gs[ra], Gb = Gs[rb];
 #pragma unroll
     for (int n = 0; n < 8; ++n) {
+      if (n > 2 * warp + 1) break;  // above the diagonal block: nothing is read there
       const int c = n * 8 + 2 * (lane & 3);
-      const double G0 = Gs[c], G1 = Gs[c + 1];
+      const float2 G0 = Gs[c], G1 = Gs[c + 1];
       float d[4] = {0.f, 0.f, 0.f, 0.f};
-      if (c <= ra) d[0] = expf(static_cast<float>(Ga - G0));
-      if (c + 1 <= ra) d[1] = expf(static_cast<float>(Ga - G1));
-      if (c <= rb) d[2] = expf(static_cast<float>(Gb - G0));
-      if (c + 1 <= rb) d[3] = expf(static_cast<float>(Gb - G1));
+      if (c <= ra) d[0] = decay_between(Ga, G0);
+      if (c + 1 <= ra) d[1] = decay_between(Ga, G1);
+      if (c <= rb) d[2] = decay_between(Gb, G0);
+      if (c + 1 <= rb) d[3] = decay_between(Gb, G1);
       float p[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) p[e] = d[e] != 0.f ? qk[n][e] * d[e] : 0.f;
@@ -133,7 +135,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(const __gri
           make_float2(c < ra ? kk[n][0] * d[0] : 0.f, c + 1 < ra ? kk[n][1] * d[1] : 0.f);
       *reinterpret_cast<float2*>(kb + rb * kKbLd + c) =
           make_float2(c < rb ? kk[n][2] * d[2] : 0.f, c + 1 < rb ? kk[n][3] * d[3] : 0.f);
-      if (n <= 2 * warp + 1) {
+      {
         uint32_t pa[3], pb[3];
         split3(p[0], p[1], pa);
         split3(p[2], p[3], pb);
@@ -150,12 +152,16 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(const __gri
     // four rows l whose number has its parity
     {
       const int j = tid >> 1, par = tid & 1;
+      const float* sub = kb + i0 * kKbLd + i0;  // rows and columns from the diagonal block on
+      const float* beta = scal + i0;
+      const int jj = j - i0;
       float x[32];
 #pragma unroll
       for (int i = 0; i < 32; ++i) x[i] = 0.f;
 #pragma unroll
       for (int i = 0; i < 64; ++i) {
-        const float* row = kb + i * kKbLd;
+        if (i % 16 == 0 && i >= 64 - i0) break;
+        const float* row = sub + i * kKbLd;
         float s0 = 0.f, s1 = 0.f;
 #pragma unroll
         for (int m = 0; m < (i + 7) / 8; ++m) {
@@ -167,21 +173,19 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(const __gri
         }
         s0 += s1;
         s0 += __shfl_xor_sync(0xffffffffu, s0, 1);
-        const float n = row[j] - s0;
-        if (((i >> 2) & 1) == par) x[(i >> 3) * 4 + (i & 3)] = scal[i] * n;
+        const float n = i > jj ? row[jj] - s0 : 0.f;
+        if (((i >> 2) & 1) == par) x[(i >> 3) * 4 + (i & 3)] = beta[i] * n;
         // this thread's parts: the first, or the second and third
-        if ((j >> 4) <= (i >> 4)) {
-          const __nv_bfloat16 p0 = __float2bfloat16_rn(n);
-          uint8_t* dst = tiles + tri_off(i, j);
-          if (par == 0) {
-            *reinterpret_cast<__nv_bfloat16*>(dst) = p0;
-          } else {
-            const float r1 = n - __bfloat162float(p0);
-            const __nv_bfloat16 p1 = __float2bfloat16_rn(r1);
-            *reinterpret_cast<__nv_bfloat16*>(dst + kTriBytes) = p1;
-            *reinterpret_cast<__nv_bfloat16*>(dst + 2 * kTriBytes) =
-                __float2bfloat16_rn(r1 - __bfloat162float(p1));
-          }
+        const __nv_bfloat16 p0 = __float2bfloat16_rn(n);
+        uint8_t* dst = tiles + tri_off(i0 + i, j);
+        if (par == 0) {
+          *reinterpret_cast<__nv_bfloat16*>(dst) = p0;
+        } else {
+          const float r1 = n - __bfloat162float(p0);
+          const __nv_bfloat16 p1 = __float2bfloat16_rn(r1);
+          *reinterpret_cast<__nv_bfloat16*>(dst + kTriBytes) = p1;
+          *reinterpret_cast<__nv_bfloat16*>(dst + 2 * kTriBytes) =
+              __float2bfloat16_rn(r1 - __bfloat162float(p1));
         }
       }
     }

@@ -29,7 +29,7 @@ constexpr int kStripThreads = 256;  // ... and four beside them
 
 // Named barriers of a strip: among its state warps, among the others, and from one to the other
 // (bar.arrive on one side, bar.sync on the other).
-enum { kBarState = 1, kBarSide = 2, kBarA = 3, kBarB = 4, kBarsPerStrip = 4 };
+enum { kBarState = 1, kBarSide = 2, kBarA = 3, kBarB = 4, kBarC = 5, kBarsPerStrip = 5 };
 __device__ __forceinline__ void bar_arrive(int id, int nthreads) {
   asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
@@ -62,7 +62,9 @@ struct ScanExchange {
   static constexpr int kO = kY + 12 * kFragBytes;         // Y, two parts (scale gamma dO, three)
   static constexpr int kP = kO + (kBwd ? 12 : 8) * kFragBytes;  // scale P^T dO, FP32
   static constexpr int kR = kP + (kBwd ? 4096 : 0);             // Q^T (scale gamma dO), FP32
-  static constexpr int kBytes = kR + (kBwd ? KD * 64 : 0);
+  static constexpr int kL = kR + (kBwd ? KD * 64 : 0);          // lambda K D, FP32
+  static constexpr int kU = kL + (kBwd ? 4096 : 0);             // U, FP32
+  static constexpr int kBytes = kU + (kBwd ? 4096 : 0);
 };
 template <int KD, int G, bool kBwd>
 GNORM_HD constexpr int scan_smem() {
@@ -348,6 +350,22 @@ __device__ __forceinline__ uint4 turn_strip(const uint32_t f[4], uint32_t strip,
   return *reinterpret_cast<const uint4*>(generic + strip_off(piece + (me.lane & 1), me.row()));
 }
 
+// Own tokens in FP32 from a warp to the one beside it.
+__device__ __forceinline__ void put_fp32(float4* buf, const float x[2][4]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) buf[i * 32] = make_float4(x[i][0], x[i][1], x[i][2], x[i][3]);
+}
+__device__ __forceinline__ void get_fp32(float x[2][4], const float4* buf) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float4 v = buf[i * 32];
+    x[i][0] = v.x;
+    x[i][1] = v.y;
+    x[i][2] = v.z;
+    x[i][3] = v.w;
+  }
+}
+
 // Forward.  kOut: writes o and the final state.  kSave: writes every chunk's S and W for the
 // backward (which runs this pass again instead of keeping them since the forward).
 template <int KD, int G, bool kOut, bool kSave>
@@ -373,6 +391,9 @@ __global__ void __launch_bounds__(G * kStripThreads, 1)
   const int chunks = static_cast<int>((end - start + kChunk - 1) / kChunk);
   const uint32_t sbase = smem_u32(smem);
   const uint32_t ex = sbase + 2 * St::kBytes + group * Ex::kBytes;
+  // W in FP32 from a state warp to the one beside it (kSave), in the place of Y's two parts
+  float4* wbuf = reinterpret_cast<float4*>(smem + 2 * St::kBytes + group * Ex::kBytes + Ex::kO) +
+                 me.warp * 64 + lane;
 
   if (side) {
     const int tid = group * kGroupThreads + (threadIdx.x & (kGroupThreads - 1));
@@ -427,6 +448,32 @@ __global__ void __launch_bounds__(G * kStripThreads, 1)
         if (row < live)
           *reinterpret_cast<uint4*>(a.o + (t0 + row) * a.ldo + static_cast<long long>(h) * a.V + v0 +
                                     (lane & 1) * 8) = v;
+      }
+      if constexpr (kSave) {
+        // W as the three parts' tiles, turned through the own tokens of v
+        uint8_t* stage = smem + (c & 1) * St::kBytes;
+        const uint32_t sg = sbase + (c & 1) * St::kBytes;
+        const long long hs = (base + c) * a.Hv + h;
+        named_barrier_sync(bars + kBarA, kStripThreads);  // W can be read, v has been
+        float x[2][4];
+        get_fp32(x, wbuf);
+        uint32_t f[3][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint32_t p[3];
+          split3(x[i][0], x[i][1], p);
+#pragma unroll
+          for (int q = 0; q < 3; ++q) f[q][2 * i] = p[q];
+          split3(x[i][2], x[i][3], p);
+#pragma unroll
+          for (int q = 0; q < 3; ++q) f[q][2 * i + 1] = p[q];
+        }
+        uint8_t* p = a.w_ws + hs * (3LL * (a.V / 64) * kTileBytes) + (v0 / 64) * kTileBytes +
+                     tile_off(me.row(), ((v0 & 63) >> 3) + (lane & 1));
+#pragma unroll
+        for (int q = 0; q < 3; ++q)
+          *reinterpret_cast<uint4*>(p + q * (a.V / 64) * kTileBytes) =
+              turn_strip(f[q], sg + St::kV, stage + St::kV, group * 2, me);
       }
     }
     return;
@@ -485,7 +532,8 @@ __global__ void __launch_bounds__(G * kStripThreads, 1)
       y[i][3] *= lm.y;
       put_tile<3>(ex + Ex::kY, me.tile(i), lane, y[i]);
     }
-    if constexpr (kOut) bar_arrive(bars + kBarA, kStripThreads);
+    if constexpr (kSave) put_fp32(wbuf, x);
+    bar_arrive(bars + kBarA, kStripThreads);
     if constexpr (kSave) {
       uint8_t* p = a.s_ws + hs * KD * a.V * 4;
 #pragma unroll
@@ -501,26 +549,6 @@ __global__ void __launch_bounds__(G * kStripThreads, 1)
       for (int e = 0; e < 4; ++e) st[n][e] *= whole;
     named_barrier_sync(bars + kBarState, kGroupThreads);
     rank_update<KD, false>(st, ex + Ex::kY, sg + St::kK, me);
-    if constexpr (kSave) {
-      // W as the three parts' tiles, turned through the own tokens of v
-      uint32_t f[3][4];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        uint32_t p[3];
-        split3(x[i][0], x[i][1], p);
-#pragma unroll
-        for (int q = 0; q < 3; ++q) f[q][2 * i] = p[q];
-        split3(x[i][2], x[i][3], p);
-#pragma unroll
-        for (int q = 0; q < 3; ++q) f[q][2 * i + 1] = p[q];
-      }
-      uint8_t* p = a.w_ws + hs * (3LL * (a.V / 64) * kTileBytes) + (v0 / 64) * kTileBytes +
-                   tile_off(me.row(), ((v0 & 63) >> 3) + (lane & 1));
-#pragma unroll
-      for (int q = 0; q < 3; ++q)
-        *reinterpret_cast<uint4*>(p + q * (a.V / 64) * kTileBytes) =
-            turn_strip(f[q], sg + St::kV, stage + St::kV, group * 2, me);
-    }
   }
   if (kOut && a.state_out != nullptr)
     store_state<KD>(st, a.state_out + head_state, a.V, v0, me);
@@ -566,6 +594,8 @@ __global__ void __launch_bounds__(kStripThreads, 1)
   const uint32_t sbase = smem_u32(smem);
   const uint32_t ex = sbase + 2 * St::kBytes;
   float4* pbuf = reinterpret_cast<float4*>(smem + 2 * St::kBytes + Ex::kP) + me.warp * 64 + lane;
+  float4* lbuf = reinterpret_cast<float4*>(smem + 2 * St::kBytes + Ex::kL) + me.warp * 64 + lane;
+  float4* ubuf = reinterpret_cast<float4*>(smem + 2 * St::kBytes + Ex::kU) + me.warp * 64 + lane;
   float4* rbuf =
       reinterpret_cast<float4*>(smem + 2 * St::kBytes + Ex::kR) + me.warp * (KD / 32) * 32 + lane;
 
@@ -632,6 +662,48 @@ __global__ void __launch_bounds__(kStripThreads, 1)
 #pragma unroll
       for (int n = 0; n < KD / 32; ++n) rbuf[n * 32] = make_float4(r[n][0], r[n][1], r[n][2], r[n][3]);
       bar_arrive(kBarB, kStripThreads);
+      // what leaves: dv, what dX has below BF16, the row sums of b and dbeta (the own tokens of
+      // W are this warp's alone)
+      uint8_t* stage = smem + (c & 1) * St::kBytes;
+      const long long t0 = start + static_cast<long long>(c) * kChunk;
+      const int live = static_cast<int>(end - t0 < kChunk ? end - t0 : kChunk);
+      const long long hs = (base + c) * a.Hv + h;
+      float w[2][4], y[2][4];
+      get_strip(w, sg + St::kW + 2 * strip_bytes<1>(), 0, me);
+#pragma unroll
+      for (int p = 1; p >= 0; --p) {
+        get_strip(t, sg + St::kW + p * strip_bytes<1>(), 0, me);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[i][e] += t[i][e];
+      }
+      named_barrier_sync(kBarC, kStripThreads);  // lambda K D and U can be read
+      get_fp32(y, lbuf);
+      get_fp32(t, ubuf);
+      float rb[2][2], rd[2][2];
+      uint32_t xh[4], xl[4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float2 be = *reinterpret_cast<const float2*>(scal + me.token(i));
+        rb[i][0] = be.x * fmaf(y[i][0], w[i][0], y[i][2] * w[i][2]);
+        rb[i][1] = be.y * fmaf(y[i][1], w[i][1], y[i][3] * w[i][3]);
+        rd[i][0] = fmaf(t[i][0], w[i][0], t[i][2] * w[i][2]);
+        rd[i][1] = fmaf(t[i][1], w[i][1], t[i][3] * w[i][3]);
+        split2(be.x * t[i][0], be.y * t[i][1], xh[2 * i], xl[2 * i]);
+        split2(be.x * t[i][2], be.y * t[i][3], xh[2 * i + 1], xl[2 * i + 1]);
+      }
+      const int row = me.row();
+      const uint4 vh = turn_strip(xh, sg + St::kW, stage + St::kW, 0, me);
+      const uint4 vl = turn_strip(xl, sg + St::kW, stage + St::kW, 0, me);
+      *reinterpret_cast<uint4*>(a.x_ws + hs * (a.V / 64 * kTileBytes) + (v0 / 64) * kTileBytes +
+                                tile_off(row, ((v0 & 63) >> 3) + (lane & 1))) = vl;
+      if (row < live)
+        *reinterpret_cast<uint4*>(a.dv + (t0 + row) * a.lddv + static_cast<long long>(h) * a.V + v0 +
+                                  (lane & 1) * 8) = vh;
+      float* dots = a.dots + (hs * (a.V / 16) + strip) * 128;
+      strip_sums(rb, dots, me);
+      strip_sums(rd, dots + 64, me);
     }
     return;
   }
@@ -649,26 +721,13 @@ __global__ void __launch_bounds__(kStripThreads, 1)
   for (int c = chunks - 1; c >= 0; --c) {
     put_state<KD>(ex + Ex::kS, me.warp, lane, d);
     __syncthreads();
-    uint8_t* stage = smem + (c & 1) * St::kBytes;
     const uint32_t sg = sbase + (c & 1) * St::kBytes;
-    const float* scal = reinterpret_cast<const float*>(stage + St::kScal);
-    const long long t0 = start + static_cast<long long>(c) * kChunk;
-    const int live = static_cast<int>(end - t0 < kChunk ? end - t0 : kChunk);
+    const float* scal = reinterpret_cast<const float*>(smem + (c & 1) * St::kBytes + St::kScal);
     const long long hs = (base + c) * a.Hv + h;
     // lambda K D
-    float y[2][4], w[2][4], t[2][4];
+    float y[2][4];
     state_product<KD, 3>(y, ex + Ex::kS, sg + St::kK, me);
-    get_strip(w, sg + St::kW + 2 * strip_bytes<1>(), 0, me);
-#pragma unroll
-    for (int p = 1; p >= 0; --p) {
-      get_strip(t, sg + St::kW + p * strip_bytes<1>(), 0, me);
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) w[i][e] += t[i][e];
-    }
     float2 be[2];
-    float r[2][2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const float2 lm = *reinterpret_cast<const float2*>(scal + 128 + me.token(i));
@@ -677,9 +736,8 @@ __global__ void __launch_bounds__(kStripThreads, 1)
       y[i][1] *= lm.y;
       y[i][2] *= lm.x;
       y[i][3] *= lm.y;
-      r[i][0] = be[i].x * fmaf(y[i][0], w[i][0], y[i][2] * w[i][2]);
-      r[i][1] = be[i].y * fmaf(y[i][1], w[i][1], y[i][3] * w[i][3]);
     }
+    put_fp32(lbuf, y);
     named_barrier_sync(kBarA, kStripThreads);  // scale P^T dO can be read
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -695,20 +753,16 @@ __global__ void __launch_bounds__(kStripThreads, 1)
     named_barrier_sync(kBarState, kGroupThreads);
     // U = dY - N^T (beta dY)
     tri_product<true, 3, 3, 3>(y, nullptr, ex + Ex::kX, sg + St::kTri, me);
-    float r2[2][2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      r2[i][0] = fmaf(y[i][0], w[i][0], y[i][2] * w[i][2]);
-      r2[i][1] = fmaf(y[i][1], w[i][1], y[i][3] * w[i][3]);
-      // dX = beta U
+      // gamma dX, dX = beta U
       const float2 gm = *reinterpret_cast<const float2*>(scal + 64 + me.token(i));
-      y[i][0] *= be[i].x;
-      y[i][1] *= be[i].y;
-      y[i][2] *= be[i].x;
-      y[i][3] *= be[i].y;
-      const float u[4] = {gm.x * y[i][0], gm.y * y[i][1], gm.x * y[i][2], gm.y * y[i][3]};
+      const float fx = gm.x * be[i].x, fy = gm.y * be[i].y;
+      const float u[4] = {fx * y[i][0], fy * y[i][1], fx * y[i][2], fy * y[i][3]};
       put_tile<3>(ex + Ex::kY, me.tile(i), lane, u);
     }
+    put_fp32(ubuf, y);
+    bar_arrive(kBarC, kStripThreads);
     {
       uint8_t* p = a.d_ws + hs * KD * a.V * 4;
 #pragma unroll
@@ -732,27 +786,6 @@ __global__ void __launch_bounds__(kStripThreads, 1)
       d[n][1] += q.y;
       d[n][2] += q.z;
       d[n][3] += q.w;
-    }
-    // what leaves: dv, what dX has below BF16, the row sums (W's matrices of the own tokens
-    // are this warp's alone)
-    {
-      uint32_t xh[4], xl[4];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        split2(y[i][0], y[i][1], xh[2 * i], xl[2 * i]);
-        split2(y[i][2], y[i][3], xh[2 * i + 1], xl[2 * i + 1]);
-      }
-      const int row = me.row();
-      const uint4 vh = turn_strip(xh, sg + St::kW, stage + St::kW, 0, me);
-      const uint4 vl = turn_strip(xl, sg + St::kW, stage + St::kW, 0, me);
-      *reinterpret_cast<uint4*>(a.x_ws + hs * (a.V / 64 * kTileBytes) + (v0 / 64) * kTileBytes +
-                                tile_off(row, ((v0 & 63) >> 3) + (lane & 1))) = vl;
-      if (row < live)
-        *reinterpret_cast<uint4*>(a.dv + (t0 + row) * a.lddv + static_cast<long long>(h) * a.V + v0 +
-                                  (lane & 1) * 8) = vh;
-      float* dots = a.dots + (hs * (a.V / 16) + strip) * 128;
-      strip_sums(r, dots, me);
-      strip_sums(r2, dots + 64, me);
     }
   }
   if (a.dstate_in != nullptr) store_state<KD>(d, a.dstate_in + head_state, a.V, v0, me);
