@@ -14,9 +14,9 @@ namespace {
 
 constexpr int64_t kMaxTokens = (int64_t(1) << 31) - 1;  // cu_seqlens are 32-bit
 
-template <typename Kernel>
+template <typename Kernel, typename... Args>
 cudaError_t launch_grid(Kernel kernel, dim3 grid, int block, int smem, cudaStream_t stream,
-                        const DeltaArgs& a) {
+                        const Args&... args) {
   const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -29,7 +29,36 @@ cudaError_t launch_grid(Kernel kernel, dim3 grid, int block, int smem, cudaStrea
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = use_pdl() ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, a);
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// cuTensorMapEncodeTiled, fetched from the driver through the runtime (no libcuda link).
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// Boxes of 64 tokens and `box` columns of a [T, cols] tensor with row stride ld; 64 columns are
+// swizzled (tile_off).  Without tokens there is nothing to map and nothing is copied.
+bool token_map(CUtensorMap* map, const void* base, int64_t T, int64_t cols, int64_t ld, int box) {
+  static EncodeTiledFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeTiledFn>(p);
+  }();
+  if (T == 0) return true;
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(T)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
+  const cuuint32_t boxes[2] = {static_cast<cuuint32_t>(box), kChunk};
+  const cuuint32_t steps[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, boxes,
+            steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            box == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int KD>
@@ -45,44 +74,45 @@ int scan_groups(const DeltaArgs& a, int num_sms) {
 }
 
 template <int KD, int G, bool kOut, bool kSave>
-cudaError_t launch_scan_fwd(const DeltaArgs& a, cudaStream_t s) {
+cudaError_t launch_scan_fwd(const DeltaArgs& a, const DeltaMaps& m, cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>(a.V / (16 * G)), static_cast<unsigned>(a.Hv),
                   static_cast<unsigned>(a.seq.B));
   return launch_grid(delta_scan_fwd_kernel<KD, G, kOut, kSave>, grid, G * kStripThreads,
-                     scan_smem<KD, G, false>(), s, a);
+                     scan_smem<KD, G, false>(), s, a, m);
 }
 
 template <int KD>
-cudaError_t launch_scan_bwd(const DeltaArgs& a, cudaStream_t s) {
+cudaError_t launch_scan_bwd(const DeltaArgs& a, const DeltaMaps& m, cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>(a.V / 16), static_cast<unsigned>(a.Hv),
                   static_cast<unsigned>(a.seq.B));
-  return launch_grid(delta_scan_bwd_kernel<KD>, grid, kStripThreads, scan_smem<KD, 1, true>(), s, a);
+  return launch_grid(delta_scan_bwd_kernel<KD>, grid, kStripThreads, scan_smem<KD, 1, true>(), s, a,
+                     m);
 }
 
 template <int KD, int VD>
-cudaError_t launch_grad(const DeltaArgs& a, int num_sms, cudaStream_t s) {
+cudaError_t launch_grad(const DeltaArgs& a, const DeltaMaps& m, int num_sms, cudaStream_t s) {
   const long long units = a.slots * a.Hk;
   const dim3 grid(static_cast<unsigned>(units < num_sms ? units : num_sms));
-  return launch_grid(delta_grad_kernel<KD, VD>, grid, kGradThreads, GradSmem<KD, VD>::kBytes, s, a);
+  return launch_grid(delta_grad_kernel<KD, VD>, grid, kGradThreads, GradSmem<KD, VD>::kBytes, s, a, m);
 }
 
 template <int KD>
-cudaError_t run_fwd(const DeltaArgs& a, int num_sms, cudaStream_t s) {
+cudaError_t run_fwd(const DeltaArgs& a, const DeltaMaps& m, int groups, cudaStream_t s) {
   const cudaError_t e = launch_prep<KD>(a, s);
   if (e != cudaSuccess) return e;
-  return scan_groups(a, num_sms) == 1 ? launch_scan_fwd<KD, 1, true, false>(a, s)
-                                      : launch_scan_fwd<KD, 2, true, false>(a, s);
+  return groups == 1 ? launch_scan_fwd<KD, 1, true, false>(a, m, s)
+                     : launch_scan_fwd<KD, 2, true, false>(a, m, s);
 }
 
 template <int KD>
-cudaError_t run_bwd(const DeltaArgs& a, int num_sms, cudaStream_t s) {
+cudaError_t run_bwd(const DeltaArgs& a, const DeltaMaps& m, int groups, int num_sms, cudaStream_t s) {
   cudaError_t e = launch_prep<KD>(a, s);
   if (e != cudaSuccess) return e;
-  e = scan_groups(a, num_sms) == 1 ? launch_scan_fwd<KD, 1, false, true>(a, s)
-                                   : launch_scan_fwd<KD, 2, false, true>(a, s);
-  if (e == cudaSuccess) e = launch_scan_bwd<KD>(a, s);
+  e = groups == 1 ? launch_scan_fwd<KD, 1, false, true>(a, m, s)
+                  : launch_scan_fwd<KD, 2, false, true>(a, m, s);
+  if (e == cudaSuccess) e = launch_scan_bwd<KD>(a, m, s);
   if (e == cudaSuccess)
-    e = a.V == 64 ? launch_grad<KD, 64>(a, num_sms, s) : launch_grad<KD, 128>(a, num_sms, s);
+    e = a.V == 64 ? launch_grad<KD, 64>(a, m, num_sms, s) : launch_grad<KD, 128>(a, m, num_sms, s);
   return e;
 }
 
@@ -247,9 +277,15 @@ int gnorm_delta_fwd(const gnorm_delta_fwd_desc* desc, void* stream) {
   if (f.zero_tail && f.o) add_zero(&a, f.o, f.ldo, d.Hv * d.V, 2);
   DeviceInfo info;
   if ((st = device_info(&info)) != GNORM_OK) return st;
+  a.err = info.err_word;
   const cudaStream_t s = as_stream(stream);
-  const cudaError_t e =
-      d.K == 64 ? run_fwd<64>(a, info.num_sms, s) : run_fwd<128>(a, info.num_sms, s);
+  const int groups = scan_groups(a, info.num_sms);
+  DeltaMaps m{};
+  if (!token_map(&m.q, d.q, d.T, d.Hk * d.K, d.ldq, 64) ||
+      !token_map(&m.k, d.k, d.T, d.Hk * d.K, d.ldk, 64) ||
+      !token_map(&m.v, d.v, d.T, d.Hv * d.V, d.ldv, 16 * groups))
+    return GNORM_ERR_CUDA;
+  const cudaError_t e = d.K == 64 ? run_fwd<64>(a, m, groups, s) : run_fwd<128>(a, m, groups, s);
   return e == cudaSuccess ? GNORM_OK : GNORM_ERR_CUDA;
 }
 
@@ -320,8 +356,16 @@ int gnorm_delta_bwd(const gnorm_delta_bwd_desc* desc, void* stream) {
   a.err = info.err_word;
   a.slots = delta_slots(d.T, d.B);
   const cudaStream_t s = as_stream(stream);
-  const cudaError_t e =
-      d.K == 64 ? run_bwd<64>(a, info.num_sms, s) : run_bwd<128>(a, info.num_sms, s);
+  const int groups = scan_groups(a, info.num_sms);
+  DeltaMaps m{};
+  if (!token_map(&m.q, d.q, d.T, kc, d.ldq, 64) || !token_map(&m.k, d.k, d.T, kc, d.ldk, 64) ||
+      !token_map(&m.v, d.v, d.T, vc, d.ldv, 16 * groups) ||
+      !token_map(&m.do_strip, f.d_o, d.T, vc, f.lddo, 16) ||
+      !token_map(&m.do_tile, f.d_o, d.T, vc, f.lddo, 64) ||
+      !token_map(&m.dv, f.dv, d.T, vc, f.lddv, 64))
+    return GNORM_ERR_CUDA;
+  const cudaError_t e = d.K == 64 ? run_bwd<64>(a, m, groups, info.num_sms, s)
+                                  : run_bwd<128>(a, m, groups, info.num_sms, s);
   return e == cudaSuccess ? GNORM_OK : GNORM_ERR_CUDA;
 }
 

@@ -132,6 +132,15 @@ __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 
+// Tensor maps over [T, heads x dim] tensors: boxes of 64 tokens, of 64 columns in the layout of
+// tile_off, or of a scan's strips of columns as plain rows.  Rows behind the tensor's end arrive
+// as zeros; rows behind a sequence's end are the next one's and are cleared after they arrive.
+struct DeltaMaps {
+  CUtensorMap q, k;         // tiles
+  CUtensorMap v, do_strip;  // strips: v (forward scans), do (backward scan)
+  CUtensorMap do_tile, dv;  // tiles
+};
+
 // ---- sequences and chunk slots.  Chunk c of sequence b has the slot base(b) + c with
 // base(b) = start(b) / 64 + b: ceil(len / 64) slots always fit before base(b + 1), so no sum
 // over the sequences is needed.  The tokens behind the last sequence are "sequence" B.
@@ -205,7 +214,7 @@ struct DeltaArgs {
   long long lddo = 0;
   uint8_t* s_ws = nullptr;  // [slots, Hv]: S before the chunk, FP32, in fragment order
   uint8_t* d_ws = nullptr;  // [slots, Hv]: the gradient of S after the chunk, likewise
-  uint8_t* w_ws = nullptr;  // [slots, Hv]: W, V/64 tiles of each of the three parts
+  uint8_t* w_ws = nullptr;  // [slots, Hv, V/16]: W's strips (delta_scan.cuh)
   uint8_t* x_ws = nullptr;  // [slots, Hv]: lo tiles of dX (dv holds hi)
   float* dots = nullptr;    // [slots, Hv, V/16, 2, 64]: each strip's share of b and dbeta
   const float* dstate_out = nullptr;
@@ -253,6 +262,17 @@ __device__ __forceinline__ void load_rows(uint32_t dst, const uint16_t* src, lon
     const int row = i / per, p = i - row * per;
     const bool ok = row < live;
     cp16(dst + (p >> 3) * kTileBytes + tile_off(row, p & 7), src + (ok ? row * ld : 0) + p * 8, ok);
+  }
+}
+// Clears rows live .. 63 of `bytes` bytes, `pitch` apart, `n` tiles of `tile` bytes; kThreads
+// threads take part.
+template <int kThreads>
+__device__ __forceinline__ void clear_rows(uint8_t* p, int bytes, int n, int tile, int live, int tid) {
+  const int per = bytes >> 4, total = (kChunk - live) * per * n;
+  for (int i = tid; i < total; i += kThreads) {
+    const int c = i / per, x = i - c * per;
+    const int t = c / (kChunk - live), r = live + c - t * (kChunk - live);
+    *reinterpret_cast<uint4*>(p + t * tile + r * bytes + x * 16) = make_uint4(0u, 0u, 0u, 0u);
   }
 }
 // Copies contiguous bytes (a multiple of 16).

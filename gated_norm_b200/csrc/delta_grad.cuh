@@ -32,6 +32,7 @@
 #pragma once
 
 #include "delta_common.cuh"
+#include "delta_scan.cuh"
 #include "tcgen05.cuh"
 
 namespace gnorm {
@@ -56,7 +57,7 @@ struct GradSmem {
   // per item, twice: decay sums [64], beta, gamma, lambda, e^{G_C}, b and dbeta sums
   static constexpr int kItem = 512 + 1024 + 512;
   static constexpr int kWork = kScal + 2 * kItem;  // sums within an item
-  static constexpr int kBytes = kWork + (3 * 512 + 16) * 4 + 64 + 1024;  // 1024: alignment
+  static constexpr int kBytes = kWork + (3 * 512 + 16) * 4 + 80 + 1024;  // 1024: alignment
 };
 
 // What a CTA works on: a chunk and key head with live tokens, and one of its value heads.
@@ -67,7 +68,7 @@ struct GradItem {
 static_assert(sizeof(GradItem) <= 48, "the next item's place");
 
 template <int KD, int VD>
-__global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __grid_constant__ DeltaArgs a) {
+__global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_constant__ DeltaMaps maps) {
   using L = GradSmem<KD, VD>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   constexpr int kVT = VD / 64, kKT = KD / 64;
@@ -91,7 +92,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
   float* red = rowsum + 512;                                        // [16]
   uint64_t* bar = reinterpret_cast<uint64_t*>(red + 16);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 1);
-  GradItem* next = reinterpret_cast<GradItem*>(bar + 2);
+  uint64_t* full = bar + 2;
+  GradItem* next = reinterpret_cast<GradItem*>(bar + 4);
 
   grid_dependency_wait();
   allow_dependent_launch();
@@ -125,28 +127,38 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
 
   // two neighbouring column tiles of a strip per warp and step
   auto pair_off = [&](int i) { return ((warp + i * (kGradThreads / 32)) * 2) * 32 + lane; };
+  // one thread's copies, and every thread's pieces of W
   auto load_tiles = [&](const GradItem& it, int qk_buf) {
     const int h = it.hk * group + it.r;
     const long long hs = it.slot * a.Hv + h;
-    if (it.r == 0) {
+    const int t0 = static_cast<int>(it.t0);
+    uint8_t* base = smem + L::kA;
+    if (tid == 0) {
+      mbar_arrive_expect_tx(full, (3 * kVT + (it.r == 0 ? 2 * kKT : 0)) * kTileBytes);
 #pragma unroll
-      for (int kt = 0; kt < kKT; ++kt) {
-        const long long col = static_cast<long long>(it.hk) * KD + kt * 64;
-        const uint32_t at = s0 + L::kQK + qk_buf * L::kQKBytes + kt * 2 * kTileBytes;
-        load_rows<kGradThreads>(at, a.q + it.t0 * a.ldq + col, a.ldq, 64, it.live, tid);
-        load_rows<kGradThreads>(at + kTileBytes, a.k + it.t0 * a.ldk + col, a.ldk, 64, it.live, tid);
+      for (int vt = 0; vt < kVT; ++vt) {
+        uint8_t* at = base + vt * 5 * kTileBytes;
+        tma_load_2d(at, &maps.do_tile, h * VD + vt * 64, t0, full);
+        tma_load_2d(at + kTileBytes, &maps.dv, h * VD + vt * 64, t0, full);
+        bulk_copy_g2s(at + 2 * kTileBytes, a.x_ws + (hs * kVT + vt) * kTileBytes, kTileBytes, full);
+      }
+      if (it.r == 0) {
+        uint8_t* qk = smem + L::kQK + qk_buf * L::kQKBytes;
+#pragma unroll
+        for (int kt = 0; kt < kKT; ++kt) {
+          tma_load_2d(qk + kt * 2 * kTileBytes, &maps.q, it.hk * KD + kt * 64, t0, full);
+          tma_load_2d(qk + (kt * 2 + 1) * kTileBytes, &maps.k, it.hk * KD + kt * 64, t0, full);
+        }
       }
     }
 #pragma unroll
     for (int vt = 0; vt < kVT; ++vt) {
+      // two of W's three parts, from strips of 16 columns: a 16-byte piece per thread and part
       const uint32_t at = s0 + L::kA + vt * 5 * kTileBytes;
-      const long long col = static_cast<long long>(h) * VD + vt * 64;
-      load_rows<kGradThreads>(at, a.dout + it.t0 * a.lddo + col, a.lddo, 64, it.live, tid);
-      load_rows<kGradThreads>(at + kTileBytes, a.dv + it.t0 * a.lddv + col, a.lddv, 64, it.live, tid);
-      load_flat<kGradThreads>(at + 2 * kTileBytes, a.x_ws + (hs * kVT + vt) * kTileBytes, kTileBytes, tid);
-      const uint8_t* w = a.w_ws + (hs * 3 * kVT + vt) * kTileBytes;
-      load_flat<kGradThreads>(at + 3 * kTileBytes, w, kTileBytes, tid);
-      load_flat<kGradThreads>(at + 4 * kTileBytes, w + kVT * kTileBytes, kTileBytes, tid);
+      const int r = tid >> 3, p = tid & 7;
+      const uint8_t* w = a.w_ws + (hs * (VD / 16) + vt * 4 + (p >> 1)) * (3LL * kStripBytes) + strip_off(p & 1, r);
+      cp16(at + 3 * kTileBytes + tile_off(r, p), w, true);
+      cp16(at + 4 * kTileBytes + tile_off(r, p), w + kStripBytes, true);
     }
     cp_commit();
   };
@@ -188,12 +200,13 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
     }
   };
 
-  load_tiles(cur, 0);
   if (warp == 0) tmem_alloc(tslot, 512);
-  if (tid == 32) {
+  if (tid == 0) {
     mbar_init(bar, 1);
+    mbar_init(full, 1);
     fence_barrier_init();
   }
+  load_tiles(cur, 0);
   if (warp < 4) load_scalars(cur, 0, warp);
   tc_fence_before();
   __syncthreads();
@@ -201,7 +214,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
   const uint32_t tmem = *tslot;
   const uint32_t mine = tmem + (static_cast<uint32_t>(warp & 3) << 21);  // this warp's lanes
   const uint32_t aA = s0 + L::kA, big = s0 + L::kBig;
-  uint32_t phase = 0;
+  uint32_t phase = 0, arrived = 0;
   bool alive = true;
   auto wait_mma = [&]() {
     if (alive) alive = mbar_spin(bar, phase, a.err, kErrWaitMma);
@@ -249,6 +262,15 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
     }
     state_tiles(sv);
     cp_wait<0>();
+    if (alive) alive = mbar_spin(full, arrived, a.err, kErrWaitFull);
+    arrived ^= 1u;
+    if (cur.live < kChunk) {
+#pragma unroll
+      for (int vt = 0; vt < kVT; ++vt)
+        clear_rows<kGradThreads>(smem + L::kA + vt * 5 * kTileBytes, 128, 2, kTileBytes, cur.live, tid);
+      if (cur.r == 0)
+        clear_rows<kGradThreads>(smem + L::kQK + qk_buf * L::kQKBytes, 128, 2 * kKT, kTileBytes, cur.live, tid);
+    }
     fence_smem_to_async();
     tc_fence_before();
     __syncthreads();

@@ -12,7 +12,7 @@
 // warp.  Each intermediate goes from accumulators to the other warps as ready left operands
 // through shared memory, one barrier of the group per product.  Four more warps per strip, one
 // beside each of the others on its scheduler, take what the way from state to state does not
-// need: the copies of the right operands (q, k, N, P tiles, double-buffered), in the forward
+// need: the copies of the right operands (q, k, N, P, double-buffered), in the forward
 // the output, in the backward the terms of dO.
 //
 // The tensor cores of the fifth generation take at least 64 rows an instruction: a head's 128
@@ -21,6 +21,7 @@
 #pragma once
 
 #include "delta_common.cuh"
+#include "tcgen05.cuh"
 
 namespace gnorm {
 
@@ -34,23 +35,23 @@ __device__ __forceinline__ void bar_arrive(int id, int nthreads) {
   asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
 
-// Strips of `G` groups, as 8 x 8 matrices [piece of 8 columns][tile of 8 tokens].
-template <int G>
-GNORM_HD constexpr int strip_bytes() { return G * 2048; }
+// A strip of W (16 columns): the three parts, each as 8 x 8 matrices [piece of 8 columns][tile
+// of 8 tokens], in the workspace as in shared memory.
+constexpr int kStripBytes = 2048;
 __device__ __forceinline__ uint32_t strip_off(int piece, int token) {
   return static_cast<uint32_t>(((piece * 8 + (token >> 3)) * 8 + (token & 7)) * 16);
 }
 
-// Shared memory of a CTA: two stages, then each group's exchange buffers.
+// Shared memory of a CTA: two stages, then each group's exchange buffers, then two barriers.
 template <int KD, int G, bool kBwd>
 struct ScanStage {
   static constexpr int kQ = 0;
   static constexpr int kK = KD / 64 * kTileBytes;
   static constexpr int kTri = 2 * kK;  // N, then P (three parts each)
   static constexpr int kScal = kTri + 6 * kTriBytes;
-  static constexpr int kV = kScal + 1024;               // v (forward) or do (backward)
-  static constexpr int kW = kV + strip_bytes<G>();      // W's three parts (backward)
-  static constexpr int kBytes = kW + (kBwd ? 3 * strip_bytes<G>() : 0);
+  static constexpr int kV = kScal + 1024;   // v (forward) or do (backward): rows of 16 G columns
+  static constexpr int kW = kV + G * 2048;  // W's three parts (backward)
+  static constexpr int kBytes = kW + (kBwd ? 3 * kStripBytes : 0);
 };
 constexpr int kFragBytes = 512;  // left operand of one 16 x 16 block, one part
 template <int KD, bool kBwd>
@@ -68,7 +69,7 @@ struct ScanExchange {
 };
 template <int KD, int G, bool kBwd>
 GNORM_HD constexpr int scan_smem() {
-  return 2 * ScanStage<KD, G, kBwd>::kBytes + G * ScanExchange<KD, kBwd>::kBytes;
+  return 2 * ScanStage<KD, G, kBwd>::kBytes + G * ScanExchange<KD, kBwd>::kBytes + 16 + 1024;  // 1024: alignment
 }
 
 // Fragment order of a 16 x K strip of FP32 values: tile n (8 columns), lane, four values.
@@ -92,14 +93,18 @@ struct ScanLane {
   __device__ __forceinline__ int tile(int i) const { return i == 0 ? warp : 7 - warp; }
   // token of column e (0, 1) of this lane in own tile i
   __device__ __forceinline__ int token(int i) const { return tile(i) * 8 + 2 * (lane & 3); }
-  // right operand: rows are the own tokens of a [64, KD] tile
+  // right operand: rows are the own tokens of a 64 x 64 tile
   __device__ __forceinline__ uint32_t rows(uint32_t t, int col0) const {
-    const int row = tile(lane >> 4) * 8 + (lane & 7);
-    return t + tile_off(row, (col0 >> 3) + ((lane >> 3) & 1));
+    return t + tile_off(tile(lane >> 4) * 8 + (lane & 7), (col0 >> 3) + ((lane >> 3) & 1));
   }
-  // the own tokens of a strip (its columns at `piece`)
-  __device__ __forceinline__ uint32_t strip(uint32_t s, int piece) const {
-    return s + strip_off(piece + ((lane >> 3) & 1), tile(lane >> 4) * 8 + (lane & 7));
+  // the own tokens of a strip of v or do, whose columns start `col` bytes into a row
+  template <int G>
+  __device__ __forceinline__ uint32_t strip(uint32_t s, int col) const {
+    return s + (tile(lane >> 4) * 8 + (lane & 7)) * (G * 32) + ((lane >> 3) & 1) * 16 + col;
+  }
+  // the own tokens of a part of W
+  __device__ __forceinline__ uint32_t wstrip(uint32_t s) const {
+    return s + strip_off((lane >> 3) & 1, tile(lane >> 4) * 8 + (lane & 7));
   }
   // 16-byte piece `lane & 1` of own token `lane / 2`
   __device__ __forceinline__ int row() const { return tile(lane >> 4) * 8 + ((lane >> 1) & 7); }
@@ -162,10 +167,13 @@ template <int KD, int kParts>
 __device__ __forceinline__ void state_product(float acc[2][4], uint32_t sbuf, uint32_t tiles,
                                               const ScanLane& me) {
   float x[kParts][2][4];
+  uint32_t rows[4];  // the swizzled addresses of a tile's four column blocks
+#pragma unroll
+  for (int i = 0; i < 4; ++i) rows[i] = me.rows(tiles, i * 16);
 #pragma unroll
   for (int kb = 0; kb < KD / 16; ++kb) {
     uint32_t b[4];
-    ldsm4(b, me.rows(tiles + (kb >> 2) * kTileBytes, (kb & 3) * 16));
+    ldsm4(b, rows[kb & 3] + (kb >> 2) * kTileBytes);
 #pragma unroll
     for (int p = 0; p < kParts; ++p) {
       uint32_t a[4];
@@ -253,14 +261,17 @@ template <int KD, bool kNeg>
 __device__ __forceinline__ void rank_update(float st[KD / 32][4], uint32_t abuf, uint32_t tiles,
                                             const ScanLane& me) {
   constexpr int kNB = KD / 64;
+  uint32_t rows[kNB];
+#pragma unroll
+  for (int nb = 0; nb < kNB; ++nb) {
+    const int col = (me.warp * kNB + nb) * 16;
+    rows[nb] = addr_bt(tiles + (col >> 6) * kTileBytes, 0, col & 63, me.lane);
+  }
 #pragma unroll
   for (int kb = 0; kb < 4; ++kb) {
     uint32_t b[kNB][4];
 #pragma unroll
-    for (int nb = 0; nb < kNB; ++nb) {
-      const int col = (me.warp * kNB + nb) * 16;
-      ldsm4t(b[nb], addr_bt(tiles + (col >> 6) * kTileBytes, kb * 16, col & 63, me.lane));
-    }
+    for (int nb = 0; nb < kNB; ++nb) ldsm4t(b[nb], rows[nb] + kb * 2048);  // 16 tokens further
 #pragma unroll
     for (int p = 0; p < 3; ++p) {
       uint32_t a[4];
@@ -275,26 +286,6 @@ __device__ __forceinline__ void rank_update(float st[KD / 32][4], uint32_t abuf,
         mma16816(st[2 * nb + 1], a, b[nb][2], b[nb][3]);
       }
     }
-  }
-}
-
-// Copies `live` rows of 2 G pieces into strip matrices, zero below.
-template <int kThreads, int G>
-__device__ __forceinline__ void load_strips(uint32_t dst, const uint16_t* src, long long ld,
-                                            int live, int tid) {
-  for (int i = tid; i < kChunk * 2 * G; i += kThreads) {
-    const int row = i / (2 * G), p = i - row * 2 * G;
-    const bool ok = row < live;
-    cp16(dst + strip_off(p, row), src + (ok ? row * ld : 0) + p * 8, ok);
-  }
-}
-// The same from a swizzled 64 x 64 tile, its columns from `piece` on.
-template <int kThreads, int G>
-__device__ __forceinline__ void load_strips_tile(uint32_t dst, const uint8_t* tile, int piece,
-                                                 int tid) {
-  for (int i = tid; i < kChunk * 2 * G; i += kThreads) {
-    const int row = i / (2 * G), p = i - row * 2 * G;
-    cp16(dst + strip_off(p, row), tile + tile_off(row, piece + p), true);
   }
 }
 
@@ -326,11 +317,10 @@ __device__ __forceinline__ void store_state(const float st[KD / 32][4], float* p
   }
 }
 
-// Own tokens of a strip in shared memory as FP32 in accumulator layout.
-__device__ __forceinline__ void get_strip(float x[2][4], uint32_t strip, int piece,
-                                          const ScanLane& me) {
+// Own tokens of a strip (address of this lane's matrix row) as FP32 in accumulator layout.
+__device__ __forceinline__ void get_strip(float x[2][4], uint32_t addr) {
   uint32_t f[4];
-  ldsm4t(f, me.strip(strip, piece));
+  ldsm4t(f, addr);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     x[i][0] = bf_lo(f[2 * i]);
@@ -340,14 +330,13 @@ __device__ __forceinline__ void get_strip(float x[2][4], uint32_t strip, int pie
   }
 }
 
-// Own tokens as BF16 pairs through the strip matrices (this warp's alone): the 16 bytes of
-// token me.row(), piece lane & 1.
-__device__ __forceinline__ uint4 turn_strip(const uint32_t f[4], uint32_t strip, uint8_t* generic,
-                                            int piece, const ScanLane& me) {
+// Own tokens as BF16 pairs through shared memory that is this warp's alone (`addr`: this lane's
+// matrix row, `own`: where it then finds the 16 bytes of token me.row(), piece lane & 1).
+__device__ __forceinline__ uint4 turn_strip(const uint32_t f[4], uint32_t addr, const uint8_t* own) {
   __syncwarp();
-  stsm4t(me.strip(strip, piece), f);
+  stsm4t(addr, f);
   __syncwarp();
-  return *reinterpret_cast<const uint4*>(generic + strip_off(piece + (me.lane & 1), me.row()));
+  return *reinterpret_cast<const uint4*>(own);
 }
 
 // Own tokens in FP32 from a warp to the one beside it.
@@ -370,11 +359,11 @@ __device__ __forceinline__ void get_fp32(float x[2][4], const float4* buf) {
 // backward (which runs this pass again instead of keeping them since the forward).
 template <int KD, int G, bool kOut, bool kSave>
 __global__ void __launch_bounds__(G * kStripThreads, 1)
-    delta_scan_fwd_kernel(const __grid_constant__ DeltaArgs a) {
+    delta_scan_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constant__ DeltaMaps maps) {
   using St = ScanStage<KD, G, false>;
   using Ex = ScanExchange<KD, false>;
-  constexpr int kLoaders = G * kGroupThreads;
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int group = threadIdx.x / kStripThreads;
   const bool side = (threadIdx.x & kGroupThreads) != 0;
   const ScanLane me((threadIdx.x >> 5) & 3, threadIdx.x & 31);
@@ -395,29 +384,51 @@ __global__ void __launch_bounds__(G * kStripThreads, 1)
   float4* wbuf = reinterpret_cast<float4*>(smem + 2 * St::kBytes + group * Ex::kBytes + Ex::kO) +
                  me.warp * 64 + lane;
 
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + 2 * St::kBytes + G * Ex::kBytes);
+  if (threadIdx.x == 0) {
+    mbar_init(&full[0], 1);
+    mbar_init(&full[1], 1);
+    fence_barrier_init();
+  }
+  __syncthreads();
+
   if (side) {
     const int tid = group * kGroupThreads + (threadIdx.x & (kGroupThreads - 1));
-    auto issue = [&](int c) {
-      const uint32_t st = sbase + (c & 1) * St::kBytes;
-      const long long t0 = start + static_cast<long long>(c) * kChunk;
-      const int live = static_cast<int>(end - t0 < kChunk ? end - t0 : kChunk);
-      load_rows<kLoaders>(st + St::kK, a.k + t0 * a.ldk + static_cast<long long>(hk) * KD, a.ldk, KD,
-                          live, tid);
+    auto issue = [&](int c) {  // one thread
+      uint8_t* st = smem + (c & 1) * St::kBytes;
+      uint64_t* bar = &full[c & 1];
+      const int t0 = static_cast<int>(start + static_cast<long long>(c) * kChunk);
+      mbar_arrive_expect_tx(bar, (kOut ? 5 : 3) * kTriBytes + 784 + (kOut ? 2 : 1) * St::kK + G * 2048);
       const uint8_t* prep = a.prep + ((base + c) * a.Hv + h) * kPrepBytes;
-      load_flat<kLoaders>(st + St::kTri, prep, (kOut ? 5 : 3) * kTriBytes, tid);
-      load_flat<kLoaders>(st + St::kScal, prep + kPrepTri, 784, tid);
-      load_strips<kLoaders, G>(st + St::kV, a.v + t0 * a.ldv + static_cast<long long>(h) * a.V + vc,
-                               a.ldv, live, tid);
-      if constexpr (kOut)
-        load_rows<kLoaders>(st + St::kQ, a.q + t0 * a.ldq + static_cast<long long>(hk) * KD, a.ldq,
-                            KD, live, tid);
-      cp_commit();
+#pragma unroll
+      for (int kt = 0; kt < KD / 64; ++kt)
+        tma_load_2d(st + St::kK + kt * kTileBytes, &maps.k, hk * KD + kt * 64, t0, bar);
+      tma_load_2d(st + St::kV, &maps.v, h * a.V + vc, t0, bar);
+      bulk_copy_g2s(st + St::kScal, prep + kPrepTri, 784, bar);
+      bulk_copy_g2s(st + St::kTri, prep, (kOut ? 5 : 3) * kTriBytes, bar);
+      if constexpr (kOut) {
+#pragma unroll
+        for (int kt = 0; kt < KD / 64; ++kt)
+          tma_load_2d(st + St::kQ + kt * kTileBytes, &maps.q, hk * KD + kt * 64, t0, bar);
+      }
     };
-    if (chunks > 0) issue(0);
+    bool alive = true;
+    if (chunks > 0 && tid == 0) issue(0);
     for (int c = 0; c < chunks; ++c) {
-      cp_wait<0>();
+      const long long left = end - start - static_cast<long long>(c) * kChunk;
+      if ((tid < 32 || left < kChunk) && alive)
+        alive = mbar_spin(&full[c & 1], (c >> 1) & 1, a.err, kErrWaitFull);
+      if (left < kChunk) {
+        uint8_t* st = smem + (c & 1) * St::kBytes;
+        const int live = static_cast<int>(left);
+        clear_rows<G * kGroupThreads>(st + St::kK, 128, KD / 64, kTileBytes, live, tid);
+        if constexpr (kOut) clear_rows<G * kGroupThreads>(st + St::kQ, 128, KD / 64, kTileBytes, live, tid);
+        clear_rows<G * kGroupThreads>(st + St::kV, G * 32, 1, 0, live, tid);
+      }
+      // what this thread wrote into the other stage comes before the copies into it
+      fence_smem_to_async();
       __syncthreads();  // stage c has arrived, the other one is free, the state can be read
-      if (c + 1 < chunks) issue(c + 1);
+      if (c + 1 < chunks && tid == 0) issue(c + 1);
       if constexpr (kOut) {
         uint8_t* stage = smem + (c & 1) * St::kBytes;
         const uint32_t sg = sbase + (c & 1) * St::kBytes;
@@ -443,8 +454,9 @@ __global__ void __launch_bounds__(G * kStripThreads, 1)
           f[2 * i] = pack_bf16x2(a.scale * o[i][0], a.scale * o[i][1]);
           f[2 * i + 1] = pack_bf16x2(a.scale * o[i][2], a.scale * o[i][3]);
         }
-        const uint4 v = turn_strip(f, sg + St::kV, stage + St::kV, group * 2, me);
         const int row = me.row();
+        const uint4 v = turn_strip(f, me.strip<G>(sg + St::kV, group * 32),
+                                   stage + St::kV + row * (G * 32) + group * 32 + (lane & 1) * 16);
         if (row < live)
           *reinterpret_cast<uint4*>(a.o + (t0 + row) * a.ldo + static_cast<long long>(h) * a.V + v0 +
                                     (lane & 1) * 8) = v;
@@ -468,12 +480,13 @@ __global__ void __launch_bounds__(G * kStripThreads, 1)
 #pragma unroll
           for (int q = 0; q < 3; ++q) f[q][2 * i + 1] = p[q];
         }
-        uint8_t* p = a.w_ws + hs * (3LL * (a.V / 64) * kTileBytes) + (v0 / 64) * kTileBytes +
-                     tile_off(me.row(), ((v0 & 63) >> 3) + (lane & 1));
+        uint8_t* p = a.w_ws + (hs * (a.V / 16) + strip) * (3LL * kStripBytes) +
+                     strip_off(lane & 1, me.row());
 #pragma unroll
         for (int q = 0; q < 3; ++q)
-          *reinterpret_cast<uint4*>(p + q * (a.V / 64) * kTileBytes) =
-              turn_strip(f[q], sg + St::kV, stage + St::kV, group * 2, me);
+          *reinterpret_cast<uint4*>(p + q * kStripBytes) =
+              turn_strip(f[q], me.strip<G>(sg + St::kV, group * 32),
+                         stage + St::kV + me.row() * (G * 32) + group * 32 + (lane & 1) * 16);
       }
     }
     return;
@@ -500,7 +513,7 @@ __global__ void __launch_bounds__(G * kStripThreads, 1)
     // X = V - gamma K S
     float x[2][4], y[2][4];
     state_product<KD, 3>(x, sbuf, sg + St::kK, me);
-    get_strip(y, sg + St::kV, group * 2, me);
+    get_strip(y, me.strip<G>(sg + St::kV, group * 32));
     float2 be[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -576,10 +589,11 @@ __device__ __forceinline__ void strip_sums(float r[2][2], float* out, const Scan
 // row sums.
 template <int KD>
 __global__ void __launch_bounds__(kStripThreads, 1)
-    delta_scan_bwd_kernel(const __grid_constant__ DeltaArgs a) {
+    delta_scan_bwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constant__ DeltaMaps maps) {
   using St = ScanStage<KD, 1, true>;
   using Ex = ScanExchange<KD, true>;
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const bool side = threadIdx.x >= kGroupThreads;
   const ScanLane me((threadIdx.x >> 5) & 3, threadIdx.x & 31);
   const int lane = me.lane;
@@ -599,32 +613,49 @@ __global__ void __launch_bounds__(kStripThreads, 1)
   float4* rbuf =
       reinterpret_cast<float4*>(smem + 2 * St::kBytes + Ex::kR) + me.warp * (KD / 32) * 32 + lane;
 
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + 2 * St::kBytes + Ex::kBytes);
+  if (threadIdx.x == 0) {
+    mbar_init(&full[0], 1);
+    mbar_init(&full[1], 1);
+    fence_barrier_init();
+  }
+  __syncthreads();
+
   if (side) {
     const int tid = threadIdx.x - kGroupThreads;
-    auto issue = [&](int c) {
-      const uint32_t st = sbase + (c & 1) * St::kBytes;
-      const long long t0 = start + static_cast<long long>(c) * kChunk;
-      const int live = static_cast<int>(end - t0 < kChunk ? end - t0 : kChunk);
+    auto issue = [&](int c) {  // one thread
+      uint8_t* st = smem + (c & 1) * St::kBytes;
+      uint64_t* bar = &full[c & 1];
+      const int t0 = static_cast<int>(start + static_cast<long long>(c) * kChunk);
       const long long hs = (base + c) * a.Hv + h;
-      load_strips<kGroupThreads, 1>(
-          st + St::kV, a.dout + t0 * a.lddo + static_cast<long long>(h) * a.V + v0, a.lddo, live, tid);
+      mbar_arrive_expect_tx(bar, 6 * kTriBytes + 784 + 3 * kStripBytes + 2 * St::kK + 2048);
       const uint8_t* prep = a.prep + hs * kPrepBytes;
-      load_flat<kGroupThreads>(st + St::kTri, prep, 6 * kTriBytes, tid);
-      load_flat<kGroupThreads>(st + St::kScal, prep + kPrepTri, 784, tid);
-      load_rows<kGroupThreads>(st + St::kK, a.k + t0 * a.ldk + static_cast<long long>(hk) * KD, a.ldk,
-                               KD, live, tid);
-      const uint8_t* w = a.w_ws + hs * (3LL * (a.V / 64) * kTileBytes) + (v0 / 64) * kTileBytes;
+      tma_load_2d(st + St::kV, &maps.do_strip, h * a.V + v0, t0, bar);
+      bulk_copy_g2s(st + St::kTri, prep, 6 * kTriBytes, bar);
+      bulk_copy_g2s(st + St::kScal, prep + kPrepTri, 784, bar);
 #pragma unroll
-      for (int p = 0; p < 3; ++p)
-        load_strips_tile<kGroupThreads, 1>(st + St::kW + p * strip_bytes<1>(),
-                                           w + p * (a.V / 64) * kTileBytes, (v0 & 63) >> 3, tid);
-      load_rows<kGroupThreads>(st + St::kQ, a.q + t0 * a.ldq + static_cast<long long>(hk) * KD, a.ldq,
-                               KD, live, tid);
-      cp_commit();
+      for (int kt = 0; kt < KD / 64; ++kt) {
+        tma_load_2d(st + St::kK + kt * kTileBytes, &maps.k, hk * KD + kt * 64, t0, bar);
+        tma_load_2d(st + St::kQ + kt * kTileBytes, &maps.q, hk * KD + kt * 64, t0, bar);
+      }
+      bulk_copy_g2s(st + St::kW, a.w_ws + (hs * (a.V / 16) + strip) * (3LL * kStripBytes),
+                    3 * kStripBytes, bar);
     };
-    if (chunks > 0) issue(chunks - 1);
+    bool alive = true;
+    uint32_t phases = 0;  // a bit per stage
+    if (chunks > 0 && tid == 0) issue(chunks - 1);
     for (int c = chunks - 1; c >= 0; --c) {
-      cp_wait<0>();
+      const long long left = end - start - static_cast<long long>(c) * kChunk;
+      if ((tid < 32 || left < kChunk) && alive)
+        alive = mbar_spin(&full[c & 1], (phases >> (c & 1)) & 1u, a.err, kErrWaitFull);
+      if (left < kChunk) {
+        uint8_t* st = smem + (c & 1) * St::kBytes;
+        clear_rows<kGroupThreads>(st + St::kQ, 128, 2 * (KD / 64), kTileBytes, static_cast<int>(left), tid);
+        clear_rows<kGroupThreads>(st + St::kV, 32, 1, 0, static_cast<int>(left), tid);
+      }
+      phases ^= 1u << (c & 1);
+      // what this thread wrote into the other stage comes before the copies into it
+      fence_smem_to_async();
       __syncthreads();  // stage c has arrived, the other one is free, D can be read
       const uint32_t sg = sbase + (c & 1) * St::kBytes;
       const float* scal = reinterpret_cast<const float*>(smem + (c & 1) * St::kBytes + St::kScal);
@@ -632,8 +663,8 @@ __global__ void __launch_bounds__(kStripThreads, 1)
       uint32_t dof[16];
 #pragma unroll
       for (int kb = 0; kb < 4; ++kb)
-        ldsm4t(dof + 4 * kb,
-               sg + St::kV + strip_off((lane >> 3) & 1, kb * 16 + ((lane >> 4) << 3) + (lane & 7)));
+        ldsm4t(dof + 4 * kb, sg + St::kV + (kb * 16 + ((lane >> 4) << 3) + (lane & 7)) * 32 +
+                                 ((lane >> 3) & 1) * 16);
       float t[2][4];
       zero_tiles(t);
       tri_product<true, 1, 3, 3>(t, dof, 0, sg + St::kTri + 3 * kTriBytes, me);
@@ -642,9 +673,9 @@ __global__ void __launch_bounds__(kStripThreads, 1)
         pbuf[i * 32] = make_float4(a.scale * t[i][0], a.scale * t[i][1], a.scale * t[i][2],
                                    a.scale * t[i][3]);
       bar_arrive(kBarA, kStripThreads);
-      if (c > 0) issue(c - 1);
+      if (c > 0 && tid == 0) issue(c - 1);
       // Q^T (scale gamma dO)
-      get_strip(t, sg + St::kV, 0, me);
+      get_strip(t, me.strip<1>(sg + St::kV, 0));
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const float2 gm = *reinterpret_cast<const float2*>(scal + 64 + me.token(i));
@@ -669,10 +700,10 @@ __global__ void __launch_bounds__(kStripThreads, 1)
       const int live = static_cast<int>(end - t0 < kChunk ? end - t0 : kChunk);
       const long long hs = (base + c) * a.Hv + h;
       float w[2][4], y[2][4];
-      get_strip(w, sg + St::kW + 2 * strip_bytes<1>(), 0, me);
+      get_strip(w, me.wstrip(sg + St::kW + 2 * kStripBytes));
 #pragma unroll
       for (int p = 1; p >= 0; --p) {
-        get_strip(t, sg + St::kW + p * strip_bytes<1>(), 0, me);
+        get_strip(t, me.wstrip(sg + St::kW + p * kStripBytes));
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -694,8 +725,9 @@ __global__ void __launch_bounds__(kStripThreads, 1)
         split2(be.x * t[i][2], be.y * t[i][3], xh[2 * i + 1], xl[2 * i + 1]);
       }
       const int row = me.row();
-      const uint4 vh = turn_strip(xh, sg + St::kW, stage + St::kW, 0, me);
-      const uint4 vl = turn_strip(xl, sg + St::kW, stage + St::kW, 0, me);
+      const uint8_t* own = stage + St::kW + strip_off(lane & 1, row);
+      const uint4 vh = turn_strip(xh, me.wstrip(sg + St::kW), own);
+      const uint4 vl = turn_strip(xl, me.wstrip(sg + St::kW), own);
       *reinterpret_cast<uint4*>(a.x_ws + hs * (a.V / 64 * kTileBytes) + (v0 / 64) * kTileBytes +
                                 tile_off(row, ((v0 & 63) >> 3) + (lane & 1))) = vl;
       if (row < live)
