@@ -2,11 +2,15 @@
 // chunks at once: N = (I + Kb diag(beta))^-1 Kb, P and the decay factors (delta_common.cuh).
 //
 // One CTA per (chunk, key head): K K^T and Q K^T once (BF16 operands, exact, FP32 sums), then
-// for each value head of the group the decays, and N by forward substitution: column j of N
-// solves n_i = Kb_ij - sum_{l<i} Kb_il beta_l n_l.  Two neighbouring threads share a column,
-// each keeps half of its values in registers and reads the coefficients of row i from shared
-// memory (the same address for the whole warp), so no step waits for another warp.  A warp's
-// sixteen columns are zero above their diagonal block: it starts there (half of the products).
+// for each value head of the group the decays, and N by blocks of 16, in FP32.  Bound by the
+// dependent steps of the substitution, 64 if taken row by row, so only the diagonal blocks are
+// (a warp each, 16 steps: column j of N solves n_i = Kb_ij - sum_{l<i} Kb_il beta_l n_l, two
+// threads a column); the others follow as products, the 16 columns of a block column four to
+// each warp, so that no step waits for another warp:
+//
+//   R = Kb_pr - sum_{r<=q<p} Kb_pq (beta N_qr)    N_pr = R - N_pp (beta R)
+//
+// N_qr (times beta) and R live in the unused upper half of Kb.
 #pragma once
 
 #include "delta_common.cuh"
@@ -148,20 +152,17 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(const __gri
       }
     }
     __syncthreads();
-    // forward substitution, column tid / 2; this thread keeps beta_l n_l of the blocks of
-    // four rows l whose number has its parity
+    // the diagonal blocks, N in Kb's place; column tid / 2, this thread keeps beta_l n_l of the
+    // blocks of four rows l whose number has its parity
     {
-      const int j = tid >> 1, par = tid & 1;
-      const float* sub = kb + i0 * kKbLd + i0;  // rows and columns from the diagonal block on
-      const float* beta = scal + i0;
-      const int jj = j - i0;
-      float x[32];
+      const int j = tid >> 1, par = tid & 1, jj = j - i0;
+      float* sub = kb + i0 * kKbLd + i0;
+      float x[8];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) x[i] = 0.f;
+      for (int i = 0; i < 8; ++i) x[i] = 0.f;
 #pragma unroll
-      for (int i = 0; i < 64; ++i) {
-        if (i % 16 == 0 && i >= 64 - i0) break;
-        const float* row = sub + i * kKbLd;
+      for (int i = 0; i < 16; ++i) {
+        float* row = sub + i * kKbLd;
         float s0 = 0.f, s1 = 0.f;
 #pragma unroll
         for (int m = 0; m < (i + 7) / 8; ++m) {
@@ -174,11 +175,13 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(const __gri
         s0 += s1;
         s0 += __shfl_xor_sync(0xffffffffu, s0, 1);
         const float n = i > jj ? row[jj] - s0 : 0.f;
-        if (((i >> 2) & 1) == par) x[(i >> 3) * 4 + (i & 3)] = beta[i] * n;
+        if (((i >> 2) & 1) == par) x[(i >> 3) * 4 + (i & 3)] = scal[i0 + i] * n;
+        __syncwarp();  // the row has been read
         // this thread's parts: the first, or the second and third
         const __nv_bfloat16 p0 = __float2bfloat16_rn(n);
         uint8_t* dst = tiles + tri_off(i0 + i, j);
         if (par == 0) {
+          row[jj] = n;
           *reinterpret_cast<__nv_bfloat16*>(dst) = p0;
         } else {
           const float r1 = n - __bfloat162float(p0);
@@ -186,6 +189,52 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(const __gri
           *reinterpret_cast<__nv_bfloat16*>(dst + kTriBytes) = p1;
           *reinterpret_cast<__nv_bfloat16*>(dst + 2 * kTriBytes) =
               __float2bfloat16_rn(r1 - __bfloat162float(p1));
+        }
+      }
+    }
+    __syncthreads();
+    // the blocks below: this lane has row lane / 2 of a block and two of its columns
+    {
+      const int row = lane >> 1, jc = warp * 4 + (lane & 1) * 2;
+      // v -= A (16 x 16, rows of kb) B (its row k at b + k * kKbLd, times f[k] where given)
+      auto product = [&](float2& v, const float* A, const float* B, const float* f) {
+#pragma unroll
+        for (int k = 0; k < 16; k += 4) {
+          const float4 x = *reinterpret_cast<const float4*>(A + k);
+          const float xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 y = *reinterpret_cast<const float2*>(B + (k + e) * kKbLd);
+            const float c = f != nullptr ? xs[e] * f[k + e] : xs[e];
+            v.x = fmaf(-c, y.x, v.x);
+            v.y = fmaf(-c, y.y, v.y);
+          }
+        }
+      };
+#pragma unroll
+      for (int r = 0; r < 3; ++r) {
+#pragma unroll
+        for (int p = r + 1; p < 4; ++p) {
+          const float* krow = kb + (p * 16 + row) * kKbLd;  // this row of Kb_p.
+          float2 v = *reinterpret_cast<const float2*>(krow + r * 16 + jc);
+          product(v, krow + r * 16, kb + (r * 16) * kKbLd + r * 16 + jc, scal + r * 16);
+#pragma unroll
+          for (int q = r + 1; q < p; ++q)
+            product(v, krow + q * 16, kb + (r * 16) * kKbLd + q * 16 + jc, nullptr);
+          float* up = kb + (r * 16 + row) * kKbLd + p * 16 + jc;  // block (r, p)
+          const float be = scal[p * 16 + row];
+          *reinterpret_cast<float2*>(up) = make_float2(be * v.x, be * v.y);
+          __syncwarp();
+          product(v, krow + p * 16, kb + (r * 16) * kKbLd + p * 16 + jc, nullptr);
+          __syncwarp();
+          *reinterpret_cast<float2*>(up) = make_float2(be * v.x, be * v.y);
+          __syncwarp();
+          uint32_t parts[3];
+          split3(v.x, v.y, parts);
+#pragma unroll
+          for (int e = 0; e < 3; ++e)
+            *reinterpret_cast<uint32_t*>(tiles + e * kTriBytes + tri_off(p * 16 + row, r * 16 + jc)) =
+                parts[e];
         }
       }
     }
