@@ -180,6 +180,18 @@ __device__ __forceinline__ int seq_of_slot(const DeltaSeqs& s, long long slot, i
   }
   return lo;
 }
+// The z-th longest of up to 32 sequences (more: the z-th), so that the CTAs that take longest
+// start first; every lane of the warp calls.
+__device__ __forceinline__ int seq_by_length(const DeltaSeqs& s, int z, int lane) {
+  if (s.cu == nullptr || s.B > 32) return z;
+  const long long len = lane < s.B ? seq_end(s, lane) - seq_start(s, lane) : -1;
+  int rank = 0;
+  for (int j = 0; j < s.B; ++j) {
+    const long long other = __shfl_sync(0xffffffffu, len, j);
+    rank += other > len || (other == len && j < lane) ? 1 : 0;
+  }
+  return __ffs(__ballot_sync(0xffffffffu, lane < s.B && rank == z)) - 1;
+}
 inline long long delta_slots(long long T, long long B) { return T / kChunk + B + 1; }
 
 // Per (slot, value head): N and P in three parts each, then beta, gamma, lambda [64] and

@@ -369,12 +369,13 @@ __global__ void __launch_bounds__(G * kStripThreads, 1)
   const ScanLane me((threadIdx.x >> 5) & 3, threadIdx.x & 31);
   const int lane = me.lane;
   const int bars = group * kBarsPerStrip;
-  const int h = blockIdx.y, b = blockIdx.z;
+  const int h = blockIdx.y;
   const int hk = h / (a.Hv / a.Hk);
   const int vc = blockIdx.x * 16 * G;  // the CTA's first column
   const int v0 = vc + group * 16, strip = v0 / 16;
   grid_dependency_wait();
   allow_dependent_launch();
+  const int b = seq_by_length(a.seq, blockIdx.z, lane);
   const long long start = seq_start(a.seq, b), end = seq_end(a.seq, b);
   const long long base = seq_base(a.seq, b);
   const int chunks = static_cast<int>((end - start + kChunk - 1) / kChunk);
@@ -597,11 +598,12 @@ __global__ void __launch_bounds__(kStripThreads, 1)
   const bool side = threadIdx.x >= kGroupThreads;
   const ScanLane me((threadIdx.x >> 5) & 3, threadIdx.x & 31);
   const int lane = me.lane;
-  const int h = blockIdx.y, b = blockIdx.z;
+  const int h = blockIdx.y;
   const int hk = h / (a.Hv / a.Hk);
   const int v0 = blockIdx.x * 16, strip = blockIdx.x;
   grid_dependency_wait();
   allow_dependent_launch();
+  const int b = seq_by_length(a.seq, blockIdx.z, lane);
   const long long start = seq_start(a.seq, b), end = seq_end(a.seq, b);
   const long long base = seq_base(a.seq, b);
   const int chunks = static_cast<int>((end - start + kChunk - 1) / kChunk);
