@@ -165,6 +165,7 @@ class BlockRMSNormFunction(torch.autograd.Function):
         return h, z
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dh, dz):
         a, r, g, w1, w2, alpha, rstd1, rstd2 = ctx.saved_tensors
         dh = None if dh is None else dh.contiguous()

@@ -38,6 +38,13 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t
                                    const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                    CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
+// The driver call below needs a context, and a thread that has made no runtime call yet (an
+// autograd worker) has none: setting the current device binds its primary context.
+bool bind_context() {
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess;
+}
+
 // Boxes of 64 tokens and `box` columns of a [T, cols] tensor with row stride ld; 64 columns are
 // swizzled (tile_off).  Without tokens there is nothing to map and nothing is copied.
 bool token_map(CUtensorMap* map, const void* base, int64_t T, int64_t cols, int64_t ld, int box) {
@@ -281,7 +288,7 @@ int gnorm_delta_fwd(const gnorm_delta_fwd_desc* desc, void* stream) {
   const cudaStream_t s = as_stream(stream);
   const int groups = scan_groups(a, info.num_sms);
   DeltaMaps m{};
-  if (!token_map(&m.q, d.q, d.T, d.Hk * d.K, d.ldq, 64) ||
+  if (!bind_context() || !token_map(&m.q, d.q, d.T, d.Hk * d.K, d.ldq, 64) ||
       !token_map(&m.k, d.k, d.T, d.Hk * d.K, d.ldk, 64) ||
       !token_map(&m.v, d.v, d.T, d.Hv * d.V, d.ldv, 16 * groups))
     return GNORM_ERR_CUDA;
@@ -358,7 +365,8 @@ int gnorm_delta_bwd(const gnorm_delta_bwd_desc* desc, void* stream) {
   const cudaStream_t s = as_stream(stream);
   const int groups = scan_groups(a, info.num_sms);
   DeltaMaps m{};
-  if (!token_map(&m.q, d.q, d.T, kc, d.ldq, 64) || !token_map(&m.k, d.k, d.T, kc, d.ldk, 64) ||
+  if (!bind_context() || !token_map(&m.q, d.q, d.T, kc, d.ldq, 64) ||
+      !token_map(&m.k, d.k, d.T, kc, d.ldk, 64) ||
       !token_map(&m.v, d.v, d.T, vc, d.ldv, 16 * groups) ||
       !token_map(&m.do_strip, f.d_o, d.T, vc, f.lddo, 16) ||
       !token_map(&m.do_tile, f.d_o, d.T, vc, f.lddo, 64) ||

@@ -393,9 +393,12 @@ GNORM_API size_t gnorm_block_bwd_workspace_bytes(int64_t M, int64_t N);
  * sequence are not read; their rows of the outputs are left as they are, or set to zero if
  * zero_tail.  States are FP32 [B, Hv, K, V].  T < 2^31; B, Hv <= 65535.
  *
- * States, the running sums of g and everything between the BF16 inputs and the outputs are
- * held to FP32: matrix operands that are not exact in BF16 are split in two BF16 values.
- * Results are bitwise the same from run to run.
+ * States, the running sums of g and everything on the way from the BF16 inputs to a state, to
+ * dv, dbeta and dinitial_state are held to FP32: matrix operands that are not exact in BF16 are
+ * cut into three BF16 parts (24 bits).  Where a product reaches only o, dq, dk or dg, two parts
+ * (17 bits) are taken.  Results are bitwise the same from run to run.  A value that is not
+ * finite reaches its own sequence and value head only (and the tokens before it in its chunk of
+ * 64); dq and dk are shared by the value heads of a key head.
  */
 typedef struct gnorm_delta_in {
   const void* q;
@@ -442,8 +445,8 @@ GNORM_API int gnorm_delta_fwd(const gnorm_delta_fwd_desc* desc, void* stream);
  * inputs, writes dq, dk, dv (BF16; dq and dk summed over the value heads of a key head), dg
  * (FP32), dbeta (beta's type) and, unless NULL, dinitial_state.  The forward keeps nothing
  * for it: chunk states are computed again.  workspace:
- * gnorm_delta_workspace_bytes(T, B, Hv, K, V, 1) bytes (about 215 KB per 64 tokens and value
- * head at K = V = 128).
+ * gnorm_delta_workspace_bytes(T, B, Hv, K, V, 1) bytes (about 230 KB per 64 tokens and value
+ * head at K = V = 128; the forward's about 32 KB).
  */
 typedef struct gnorm_delta_bwd_desc {
   gnorm_delta_in in;
@@ -549,7 +552,7 @@ GNORM_API int gnorm_plan_query(int kind, int64_t M, int64_t N, int deterministic
 /*
  * Device-side error word: kernels set a bit here if a bounded wait inside them gave up
  * (1 = a wait for copied data, 2 = a wait for a free pipeline stage, 4 = the self-test's
- * wait, see gnorm_selftest_wait_timeout).  Synchronises the
+ * wait, see gnorm_selftest_wait_timeout, 8 = a wait for the tensor cores).  Synchronises the
  * current device, returns the word and clears it if `reset` != 0.  Returns -1 (as an int)
  * if the word cannot be read.
  */

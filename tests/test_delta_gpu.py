@@ -388,6 +388,28 @@ def test_autograd():
         close(v.grad, recurrence(y)["dv"], "dv")
 
 
+def test_first_call_of_a_thread():
+    """A thread that has made no CUDA call yet: both directions run there."""
+    import threading
+
+    x = make([70], 1, 2, 64, 64, state=True)
+    want = call(x)
+    torch.cuda.synchronize()
+    for fn in (lambda: gn.gnorm_delta_fwd(x["q"], x["k"], x["v"], x["g"], x["beta"],
+                                          initial_state=x["S0"])[:1],
+               lambda: gn.gnorm_delta_bwd(x["do"], x["q"], x["k"], x["v"], x["g"], x["beta"],
+                                          initial_state=x["S0"], dfinal_state=x["dS"])):
+        out = []
+        t = threading.Thread(target=lambda: out.append(fn()))
+        t.start()
+        t.join()
+        torch.cuda.synchronize()
+        assert len(out) == 1
+        names = ("o",) if len(out[0]) == 1 else GRADS
+        for n, got in zip(names, out[0]):
+            assert torch.equal(got, want[n]), n
+
+
 def test_gradients_against_differences():
     """The adjoint that the tests compare with, against central differences in FP64."""
     x = make([70], 1, 2, 64, 64, state=True)
