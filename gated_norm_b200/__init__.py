@@ -1,8 +1,9 @@
 """gated_norm_b200: SiLU-gated RMSNorm training kernels for B200 (sm_100a).
 
 The kernels live in ``libgnorm.so`` behind the C ABI of ``include/gnorm.h``; this package
-is a thin binding over it.  Importing the package loads the library and fails loudly if it
-has not been built (``python gated_norm_b200/build.py``): there is no CPU fallback.
+is a thin binding over it (ctypes, and the compiled module ``_marshal`` for the block norm and
+the delta rule).  Importing the package loads the library and fails loudly if it has not been
+built (``python gated_norm_b200/build.py``): there is no CPU fallback.
 """
 from .autograd import GatedRMSNorm, GatedRMSNormFunction, gated_rmsnorm  # noqa: F401
 from .block import (  # noqa: F401

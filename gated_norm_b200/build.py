@@ -1,4 +1,4 @@
-"""Build libgnorm.so in-tree with nvcc for sm_100a.
+"""Build libgnorm.so in-tree with nvcc for sm_100a, and the binding's module _marshal.so.
 
     python gated_norm_b200/build.py [--force] [--verbose]
 
@@ -8,7 +8,8 @@ Each source is compiled to an object under ``<repo>/_build/`` (in parallel), the
 into ``gated_norm_b200/libgnorm.so``.  The CUDA runtime is linked statically and its
 symbols are kept out of the library's export table, so only the ``gnorm_*`` C entry
 points are visible.  A source is recompiled when it, or any header, is newer than its
-object.
+object.  _marshal.so (csrc/binding.cpp, g++ against torch's headers) is linked to libgnorm.so
+beside it.
 """
 from __future__ import annotations
 
@@ -26,6 +27,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libgnorm.so")
+MARSHAL = os.path.join(PKG, "_marshal.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 SOURCES = ["api.cu", "fwd.cu", "bwd.cu", "plan.cpp", "noalloc.cu", "host_step.cu",
@@ -63,8 +65,33 @@ def _compile(src: str, obj: str, verbose: bool) -> str:
     return res.stdout + res.stderr
 
 
+def _build_marshal() -> None:
+    """Compile binding.cpp into the Python module; its only project header is gnorm.h."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    out = sysconfig.get_paths()
+    src = os.path.join(CSRC, "binding.cpp")
+    tmp = MARSHAL + ".tmp"
+    cmd = ["g++", "-shared", "-fPIC", "-O2", "-std=c++17", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-DTORCH_EXTENSION_NAME=_marshal", src, "-o", tmp, "-I", INCLUDE,
+           "-I", out["include"], "-I", os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
+    for inc in cpp_extension.include_paths():
+        cmd += ["-isystem", inc]
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cmd += [f"-L{lib}", "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu", "-ltorch_python",
+            f"-Wl,-rpath,{lib}", f"-L{PKG}", "-l:libgnorm.so", "-Wl,-rpath,$ORIGIN"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed for binding.cpp:\n{res.stdout}\n{res.stderr}")
+    os.replace(tmp, MARSHAL)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile and link libgnorm.so; returns its path."""
+    """Compile and link libgnorm.so and the binding's module; returns the library's path."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     newest_header = max((os.path.getmtime(h) for h in _headers()), default=0.0)
     jobs = []
@@ -89,6 +116,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if res.returncode != 0:
             raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
         os.replace(tmp, LIB)
+    if force or _stale(MARSHAL, os.path.join(CSRC, "binding.cpp"),
+                       os.path.getmtime(os.path.join(INCLUDE, "gnorm.h"))):
+        _build_marshal()
     if verbose:
         for log in logs:
             if log.strip():

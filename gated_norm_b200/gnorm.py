@@ -118,6 +118,11 @@ def _stream(stream, device):
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
+def _handle(stream):
+    """A stream as the module _marshal takes it; None = torch's current one."""
+    return None if stream is None else stream.cuda_stream
+
+
 class _Here:
     """What `with _on(device)` enters when the device is the current one already: nothing (a
     guard's two driver calls are a good part of a small call)."""
