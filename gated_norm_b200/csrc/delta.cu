@@ -1,5 +1,6 @@
 // delta.cu -- launchers and extern "C" entry points of the gated delta rule.
 #include "delta_grad.cuh"
+#include "delta_head.cuh"
 #include "delta_prep.cuh"
 #include "delta_scan.cuh"
 #include "delta_step.cuh"
@@ -103,10 +104,31 @@ cudaError_t launch_grad(const DeltaArgs& a, const DeltaMaps& m, int num_sms, cud
   return launch_grid(delta_grad_kernel<KD, VD>, grid, kGradThreads, GradSmem<KD, VD>::kBytes, s, a, m);
 }
 
+// A whole head per CTA instead of strips?  Strips need about 2850 cycles each a chunk on an SM
+// that is full of them (22800 a head of 128 columns), a whole head 7000, whose chunks follow one
+// another on one SM.  Sequences of one length (the host knows): once two heads share five SMs
+// (16384 tokens x 64 heads 1565 us against 1872; 8 x 1024 tokens x 16 heads 148 against 254; 32
+// heads of 16384 tokens 1400 against 955).  Packed sequences, of which the longest decides and
+// is often twice the mean: with more heads than SMs (8 sequences of 16384 tokens in all x 32
+// heads 582 against 889; 8 of 8192 x 16: 274 against 252).  Heads of 64 columns waste half of
+// an instruction's rows (8 of 8192 x 32, K = V = 64: 275 against 246).
+bool whole_heads(const DeltaArgs& a, int num_sms) {
+  const long long heads = static_cast<long long>(a.seq.B) * a.Hv;
+  if (a.V != 128) return false;
+  return a.seq.cu != nullptr && a.seq.B > 1 ? heads > num_sms : 5 * heads > 2LL * num_sms;
+}
+
 template <int KD>
-cudaError_t run_fwd(const DeltaArgs& a, const DeltaMaps& m, int groups, cudaStream_t s) {
+cudaError_t launch_head_fwd(const DeltaArgs& a, const DeltaMaps& m, cudaStream_t s) {
+  const dim3 grid(static_cast<unsigned>(a.Hv), static_cast<unsigned>(a.seq.B));
+  return launch_grid(delta_head_fwd_kernel<KD, 128>, grid, kHeadThreads, head_smem<KD, 128>(), s, a, m);
+}
+
+template <int KD>
+cudaError_t run_fwd(const DeltaArgs& a, const DeltaMaps& m, bool whole, int groups, cudaStream_t s) {
   const cudaError_t e = launch_prep<KD>(a, s);
   if (e != cudaSuccess) return e;
+  if (whole) return launch_head_fwd<KD>(a, m, s);
   return groups == 1 ? launch_scan_fwd<KD, 1, true, false>(a, m, s)
                      : launch_scan_fwd<KD, 2, true, false>(a, m, s);
 }
@@ -286,13 +308,15 @@ int gnorm_delta_fwd(const gnorm_delta_fwd_desc* desc, void* stream) {
   if ((st = device_info(&info)) != GNORM_OK) return st;
   a.err = info.err_word;
   const cudaStream_t s = as_stream(stream);
+  const bool whole = whole_heads(a, info.num_sms);
   const int groups = scan_groups(a, info.num_sms);
   DeltaMaps m{};
   if (!bind_context() || !token_map(&m.q, d.q, d.T, d.Hk * d.K, d.ldq, 64) ||
       !token_map(&m.k, d.k, d.T, d.Hk * d.K, d.ldk, 64) ||
-      !token_map(&m.v, d.v, d.T, d.Hv * d.V, d.ldv, 16 * groups))
+      !token_map(&m.v, d.v, d.T, d.Hv * d.V, d.ldv, whole ? 64 : 16 * groups))
     return GNORM_ERR_CUDA;
-  const cudaError_t e = d.K == 64 ? run_fwd<64>(a, m, groups, s) : run_fwd<128>(a, m, groups, s);
+  const cudaError_t e =
+      d.K == 64 ? run_fwd<64>(a, m, whole, groups, s) : run_fwd<128>(a, m, whole, groups, s);
   return e == cudaSuccess ? GNORM_OK : GNORM_ERR_CUDA;
 }
 

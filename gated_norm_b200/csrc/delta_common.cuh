@@ -96,19 +96,25 @@ __device__ __forceinline__ uint32_t addr_at(uint32_t tile, int row0, int col0, i
 __device__ __forceinline__ float bf_lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
+// What a BF16 pair leaves of two FP32 values (exact), one packed operation.
+__device__ __forceinline__ float2 left_of(float2 x, uint32_t p) {
+  return fma2(make_float2(bf_lo(p), bf_hi(p)), splat2(-1.f), x);
+}
+
 // Two FP32 values as BF16 pairs: hi, and lo = what hi leaves.
 __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
   hi = pack_bf16x2(x, y);
-  lo = pack_bf16x2(x - bf_lo(hi), y - bf_hi(hi));
+  const float2 r = left_of(make_float2(x, y), hi);
+  lo = pack_bf16x2(r.x, r.y);
 }
 
 // Two FP32 values as BF16 pairs: three parts, 24 bits.
 __device__ __forceinline__ void split3(float x, float y, uint32_t p[3]) {
   p[0] = pack_bf16x2(x, y);
-  x -= bf_lo(p[0]);
-  y -= bf_hi(p[0]);
-  p[1] = pack_bf16x2(x, y);
-  p[2] = pack_bf16x2(x - bf_lo(p[1]), y - bf_hi(p[1]));
+  float2 r = left_of(make_float2(x, y), p[0]);
+  p[1] = pack_bf16x2(r.x, r.y);
+  r = left_of(r, p[1]);
+  p[2] = pack_bf16x2(r.x, r.y);
 }
 
 // A fragments (hi, lo) of a 16 x 16 block from two accumulator tiles 16 x 8 side by side.

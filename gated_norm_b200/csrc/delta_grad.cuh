@@ -277,15 +277,14 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
     if (tid == 0) {
       tc_fence_after();
       constexpr uint32_t idS = mma_desc<false, true, KD>(), idW = mma_desc<false, false, 64>();
+      const uint64_t ad = smem_desc(aA, 16, 1024), sd = smem_desc(big, kTileBytes, 1024);
 #pragma unroll
       for (int ks = 0; ks < VD / 16; ++ks) {
-        const uint32_t at = aA + (ks >> 2) * 5 * kTileBytes + (ks & 3) * 32;
-        const uint64_t a0 = smem_desc(at, 16, 1024), a1 = smem_desc(at + kTileBytes, 16, 1024);
-        const uint32_t st = big + (ks >> 2) * kKT * kTileBytes + (ks & 3) * 2048;
-        const uint64_t sh = smem_desc(st, kTileBytes, 1024);
-        const uint64_t sl = smem_desc(st + L::kState / 2, kTileBytes, 1024);
-        const uint64_t wh = smem_desc(at + 3 * kTileBytes, 16, 1024);
-        const uint64_t wl = smem_desc(at + 4 * kTileBytes, 16, 1024);
+        const uint32_t at = (ks >> 2) * 5 * kTileBytes + (ks & 3) * 32;
+        const uint32_t st = (ks >> 2) * kKT * kTileBytes + (ks & 3) * 2048;
+        const uint64_t a0 = desc_at(ad, at), a1 = desc_at(ad, at + kTileBytes);
+        const uint64_t sh = desc_at(sd, st), sl = desc_at(sd, st + L::kState / 2);
+        const uint64_t wh = desc_at(ad, at + 3 * kTileBytes), wl = desc_at(ad, at + 4 * kTileBytes);
         tc_mma(tmem + kD1, a0, sh, idS, ks > 0);
         tc_mma(tmem + kD1, a0, sl, idS, true);
         tc_mma(tmem + kD1b, a1, sh, idS, ks > 0);
@@ -294,10 +293,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
         tc_mma(tmem + kD2b, a1, wh, idW, ks > 0);
       }
       if (cur.r == 0) {
+        const uint64_t qd = smem_desc(qk, 16, 1024);
 #pragma unroll
         for (int ks = 0; ks < KD / 16; ++ks) {
-          const uint32_t at = qk + (ks >> 2) * 2 * kTileBytes + (ks & 3) * 32;
-          tc_mma(tmem + kKK, smem_desc(at, 16, 1024), smem_desc(at + kTileBytes, 16, 1024), idW, ks > 0);
+          const uint32_t at = (ks >> 2) * 2 * kTileBytes + (ks & 3) * 32;
+          tc_mma(tmem + kKK, desc_at(qd, at), desc_at(qd, at + kTileBytes), idW, ks > 0);
         }
       }
       tc_commit(bar);
@@ -345,14 +345,14 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
     if (tid == 0) {
       tc_fence_after();
       constexpr uint32_t idS = mma_desc<false, true, KD>();
+      const uint64_t ad = smem_desc(aA, 16, 1024), sd = smem_desc(big, kTileBytes, 1024);
 #pragma unroll
       for (int ks = 0; ks < VD / 16; ++ks) {
-        const uint32_t at = aA + (ks >> 2) * 5 * kTileBytes + (ks & 3) * 32;
-        const uint32_t st = big + (ks >> 2) * kKT * kTileBytes + (ks & 3) * 2048;
-        const uint64_t wh = smem_desc(at + 2 * kTileBytes, 16, 1024);  // rows 64..127: W hi
-        const uint64_t wl = smem_desc(at + 3 * kTileBytes, 16, 1024);
-        const uint64_t dh = smem_desc(st, kTileBytes, 1024);
-        const uint64_t dl = smem_desc(st + L::kState / 2, kTileBytes, 1024);
+        const uint32_t at = (ks >> 2) * 5 * kTileBytes + (ks & 3) * 32;
+        const uint32_t st = (ks >> 2) * kKT * kTileBytes + (ks & 3) * 2048;
+        const uint64_t wh = desc_at(ad, at + 2 * kTileBytes);  // rows 64..127: W hi
+        const uint64_t wl = desc_at(ad, at + 3 * kTileBytes);
+        const uint64_t dh = desc_at(sd, st), dl = desc_at(sd, st + L::kState / 2);
         tc_mma(tmem + kD3, wh, dh, idS, ks > 0);
         tc_mma(tmem + kD3, wh, dl, idS, true);
         tc_mma(tmem + kD3, wl, dh, idS, true);
@@ -447,17 +447,19 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
     if (tid == 0) {
       tc_fence_after();
       constexpr uint32_t idP = mma_desc<false, true, KD>(), idT = mma_desc<true, true, KD>();
+      const uint64_t qd = smem_desc(qk, 2 * kTileBytes, 1024), pd = smem_desc(big, 16, 1024);
 #pragma unroll
-      for (int ks = 0; ks < 4; ++ks) {
-        const uint64_t q = smem_desc(qk + ks * 2048, 2 * kTileBytes, 1024);
-        const uint64_t k = smem_desc(qk + kTileBytes + ks * 2048, 2 * kTileBytes, 1024);
+      for (int part = 0; part < 2; ++part) {
+        const uint32_t ph = part * 2 * kTileBytes;
+        // transposed, as rows 64..127 (rows 0..63, not read, are a q tile's)
+        const uint64_t tp = smem_desc(qk, big + ph - qk, 1024);
+        const uint64_t te = smem_desc(qk, big + ph + kTileBytes - qk, 1024);
 #pragma unroll
-        for (int part = 0; part < 2; ++part) {
-          const uint32_t ph = big + part * 2 * kTileBytes;
-          tc_mma(tmem + kD4, smem_desc(ph + ks * 32, 16, 1024), k, idP, ks + part > 0);
-          // transposed, as rows 64..127 (rows 0..63, not read, are a q tile's)
-          tc_mma(tmem + kD5, smem_desc(qk + ks * 2048, ph - qk, 1024), q, idT, ks + part > 0);
-          tc_mma(tmem + kD5, smem_desc(qk + ks * 2048, ph + kTileBytes - qk, 1024), k, idT, true);
+        for (int ks = 0; ks < 4; ++ks) {
+          const uint64_t q = desc_at(qd, ks * 2048), k = desc_at(qd, kTileBytes + ks * 2048);
+          tc_mma(tmem + kD4, desc_at(pd, ph + ks * 32), k, idP, ks + part > 0);
+          tc_mma(tmem + kD5, desc_at(tp, ks * 2048), q, idT, ks + part > 0);
+          tc_mma(tmem + kD5, desc_at(te, ks * 2048), k, idT, true);
         }
       }
       tc_commit(bar);

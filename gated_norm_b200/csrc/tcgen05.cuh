@@ -1,6 +1,6 @@
-// tcgen05.cuh -- the fifth-generation tensor cores (sm_100a) as the gated delta rule's gradient
-// kernel uses them: one CTA, BF16 operands in shared memory, FP32 accumulators in tensor
-// memory, 128 rows an instruction.
+// tcgen05.cuh -- the fifth-generation tensor cores (sm_100a) as the gated delta rule's kernels
+// use them: one CTA, BF16 operands in shared memory (the left one in tensor memory too), FP32
+// accumulators in tensor memory, 128 rows an instruction.
 #pragma once
 
 #include "device_common.cuh"
@@ -33,6 +33,14 @@ __device__ __forceinline__ void fence_smem_to_async() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// The same for an operand of 8 x 8 matrices (128 contiguous bytes): `lbo` bytes from a matrix to
+// the next along the reduction, `sbo` along the rows.
+__device__ __forceinline__ uint64_t smem_desc_plain(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+  return static_cast<uint64_t>((addr & 0x3ffffu) >> 4) |
+         (static_cast<uint64_t>((lbo >> 4) & 0x3fffu) << 16) |
+         (static_cast<uint64_t>((sbo >> 4) & 0x3fffu) << 32) | (1ull << 46);
+}
+
 // Descriptor of an operand made of 64 x 64 BF16 tiles in the layout of tile_off (rows of 128
 // bytes, 16-byte pieces swizzled over eight rows; tiles 1024-byte aligned): `sbo` bytes from
 // eight rows to the next, `lbo` bytes from 64 columns to the next where the columns are the
@@ -41,6 +49,12 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint3
   return static_cast<uint64_t>((addr & 0x3ffffu) >> 4) |
          (static_cast<uint64_t>((lbo >> 4) & 0x3fffu) << 16) |
          (static_cast<uint64_t>((sbo >> 4) & 0x3fffu) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// A descriptor whose address moves by a constant: one addition in the issuing thread, whose
+// instructions between two products are what bounds small ones.
+__device__ __forceinline__ uint64_t desc_at(uint64_t desc, uint32_t bytes) {
+  return (desc & 0xffffffff00000000ull) | static_cast<uint32_t>(static_cast<uint32_t>(desc) + (bytes >> 4));
 }
 
 // Instruction descriptor: FP32 += BF16 x BF16, M = 128, N columns; kA / kB: the operand's tiles
@@ -58,6 +72,14 @@ __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint3
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+      : "memory");
+}
+// The same with A in tensor memory: lane = row, two BF16 values of the reduction a column.
+__device__ __forceinline__ void tc_mma_t(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
       : "memory");
 }
 // Arrives on `bar` when all tensor-core work this thread has issued is done.
@@ -107,6 +129,19 @@ __device__ __forceinline__ void tc_load16(uint32_t addr, float v[16]) {
       : "memory");
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// 16 columns of this warp's 32 lanes into tensor memory; tc_store_wait before they are used.
+__device__ __forceinline__ void tc_store16(uint32_t addr, const uint32_t r[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tc_store_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
 }  // namespace gnorm

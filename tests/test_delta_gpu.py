@@ -187,6 +187,69 @@ def test_many_short_sequences():
     check(make([1 + i % 5 for i in range(150)], 1, 1, 64, 64, state=True))
 
 
+def many_heads(seqs, Hv):
+    """Enough sequences and heads for a whole head per SM (heads of 128 columns)."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert seqs * Hv > sms
+    return seqs, Hv
+
+
+@pytest.mark.parametrize("K", [64, 128])
+def test_whole_heads_packed(K):
+    seqs, Hv = many_heads(40, 4)
+    lens = [(1, 64, 0, 65, 130, 3, 63, 17)[i % 8] for i in range(seqs)]
+    x = make(lens, 2, Hv, K, 128, state=True, tail=9, beta=torch.bfloat16)
+    check(x)
+    first = call(x)
+    x["v"][200, 1] = float("nan")  # in one sequence, one head
+    got = call(x)
+    b = next(i for i in range(seqs) if sum(lens[:i + 1]) > 200)
+    lo, hi = sum(lens[:b]), sum(lens[:b + 1])
+    assert torch.equal(got["o"][:lo], first["o"][:lo]) and torch.equal(got["o"][hi:], first["o"][hi:])
+    assert torch.equal(got["o"][:, [0, 2, 3]], first["o"][:, [0, 2, 3]])
+    keep = [i for i in range(seqs) if i != b]
+    assert torch.equal(got["S"][keep], first["S"][keep])
+
+
+@pytest.mark.parametrize("K,L", [(128, 1), (64, 64), (128, 129)])
+def test_whole_heads_of_one_length(K, L):
+    """The batch form, without an initial state, on two streams at once and replayed."""
+    B, Hv = many_heads(40, 4)
+    x = make([L] * B, 1, Hv, K, 128)
+    y = [x[n].unflatten(0, (B, L)) for n in ("q", "k", "v", "g", "beta")]
+    o, S = gn.gnorm_delta_fwd(*y, output_final_state=True)
+    ref = recurrence(x, grads=False)
+    close(o.flatten(0, 1), ref["o"], "o", size=ref["size"])
+    close(S, ref["S"], "S")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        o2, S2 = gn.gnorm_delta_fwd(*y, output_final_state=True)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            o4, S4 = gn.gnorm_delta_fwd(*y, output_final_state=True)
+    o3, S3 = gn.gnorm_delta_fwd(*y, output_final_state=True)
+    torch.cuda.current_stream().wait_stream(s)
+    g.replay()
+    torch.cuda.synchronize()
+    for p, q in ((o2, S2), (o3, S3), (o4, S4)):
+        assert torch.equal(p, o) and torch.equal(q, S)
+    assert gn.gnorm_device_error(reset=True) == 0
+
+
+def test_whole_heads_reset_and_repeat():
+    seqs, Hv = many_heads(40, 4)
+    x = make([70] * seqs, 1, Hv, 128, 128, state=True, decay=0.01)
+    x["k"] = x["k"][:1].expand(70 * seqs, 1, 128).contiguous()
+    x["beta"][:] = 0.9
+    x["g"][30] = float("-inf")
+    o, S = gn.gnorm_delta_fwd(x["q"], x["k"], x["v"], x["g"], x["beta"], scale=x["scale"],
+                              cu_seqlens=x["cu"], initial_state=x["S0"], output_final_state=True)
+    ref = recurrence(dict(x, g=x["g"].clamp(min=-700.0)), grads=False)
+    close(o, ref["o"], "o", size=ref["size"])
+    close(S, ref["S"], "S")
+
+
 def test_many_heads_of_one_key_head():
     check(make([97], 1, 8, 128, 128))
 
