@@ -95,8 +95,6 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
   uint64_t* full = bar + 2;
   GradItem* next = reinterpret_cast<GradItem*>(bar + 4);
 
-  grid_dependency_wait();
-  allow_dependent_launch();
   const int group = a.Hv / a.Hk;
   const long long units = a.slots * a.Hk;
   // the first unit from u on (in this CTA's steps) that has tokens
@@ -123,6 +121,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
     return it;
   };
   GradItem cur = find(blockIdx.x);
+  grid_dependency_wait();  // (the kernel before is this call's own: see delta_scan.cuh)
+  allow_dependent_launch();
   if (cur.unit >= units) return;
 
   // two neighbouring column tiles of a strip per warp and step

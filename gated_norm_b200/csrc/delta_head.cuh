@@ -92,8 +92,6 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
     *reinterpret_cast<uint4*>(p) = make_uint4(0u, 0u, 0u, 0u);
   }
   fence_smem_to_async();
-  grid_dependency_wait();
-  allow_dependent_launch();
   const int b = seq_by_length(a.seq, blockIdx.y, lane);
   const long long start = seq_start(a.seq, b), end = seq_end(a.seq, b);
   const long long base = seq_base(a.seq, b);
@@ -102,6 +100,8 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  grid_dependency_wait();  // (the kernel before is this call's own: see delta_scan.cuh)
+  allow_dependent_launch();
   const uint32_t tmem = *tslot;
   bool alive = true;
   auto wait = [&](uint64_t* bar, uint32_t parity, unsigned bit) {

@@ -15,6 +15,10 @@
 // need: the copies of the right operands (q, k, N, P, double-buffered), in the forward
 // the output, in the backward the terms of dO.
 //
+// What only the call's inputs decide (the sequence's place, its state, the first q, k and v) is
+// fetched before the wait for the kernel before, which is this call's own and has itself
+// waited for everything older.
+//
 // The tensor cores of the fifth generation take at least 64 rows an instruction: a head's 128
 // columns would be one tile on one SM, its 66000 values a chunk would be cut and scaled by
 // that SM alone, and the other SMs would wait -- the heads of a layer are fewer than the SMs.
@@ -373,8 +377,6 @@ __global__ void __launch_bounds__(G * kStripThreads, 1)
   const int hk = h / (a.Hv / a.Hk);
   const int vc = blockIdx.x * 16 * G;  // the CTA's first column
   const int v0 = vc + group * 16, strip = v0 / 16;
-  grid_dependency_wait();
-  allow_dependent_launch();
   const int b = seq_by_length(a.seq, blockIdx.z, lane);
   const long long start = seq_start(a.seq, b), end = seq_end(a.seq, b);
   const long long base = seq_base(a.seq, b);
@@ -395,26 +397,33 @@ __global__ void __launch_bounds__(G * kStripThreads, 1)
 
   if (side) {
     const int tid = group * kGroupThreads + (threadIdx.x & (kGroupThreads - 1));
-    auto issue = [&](int c) {  // one thread
+    // one thread: the call's inputs, and what the kernel before has made of them
+    auto issue_inputs = [&](int c) {
       uint8_t* st = smem + (c & 1) * St::kBytes;
       uint64_t* bar = &full[c & 1];
       const int t0 = static_cast<int>(start + static_cast<long long>(c) * kChunk);
       mbar_arrive_expect_tx(bar, (kOut ? 5 : 3) * kTriBytes + 784 + (kOut ? 2 : 1) * St::kK + G * 2048);
-      const uint8_t* prep = a.prep + ((base + c) * a.Hv + h) * kPrepBytes;
 #pragma unroll
       for (int kt = 0; kt < KD / 64; ++kt)
         tma_load_2d(st + St::kK + kt * kTileBytes, &maps.k, hk * KD + kt * 64, t0, bar);
       tma_load_2d(st + St::kV, &maps.v, h * a.V + vc, t0, bar);
-      bulk_copy_g2s(st + St::kScal, prep + kPrepTri, 784, bar);
-      bulk_copy_g2s(st + St::kTri, prep, (kOut ? 5 : 3) * kTriBytes, bar);
       if constexpr (kOut) {
 #pragma unroll
         for (int kt = 0; kt < KD / 64; ++kt)
           tma_load_2d(st + St::kQ + kt * kTileBytes, &maps.q, hk * KD + kt * 64, t0, bar);
       }
     };
+    auto issue_prep = [&](int c) {
+      uint8_t* st = smem + (c & 1) * St::kBytes;
+      const uint8_t* prep = a.prep + ((base + c) * a.Hv + h) * kPrepBytes;
+      bulk_copy_g2s(st + St::kScal, prep + kPrepTri, 784, &full[c & 1]);
+      bulk_copy_g2s(st + St::kTri, prep, (kOut ? 5 : 3) * kTriBytes, &full[c & 1]);
+    };
     bool alive = true;
-    if (chunks > 0 && tid == 0) issue(0);
+    if (chunks > 0 && tid == 0) issue_inputs(0);
+    grid_dependency_wait();
+    allow_dependent_launch();
+    if (chunks > 0 && tid == 0) issue_prep(0);
     for (int c = 0; c < chunks; ++c) {
       const long long left = end - start - static_cast<long long>(c) * kChunk;
       if ((tid < 32 || left < kChunk) && alive)
@@ -429,7 +438,10 @@ __global__ void __launch_bounds__(G * kStripThreads, 1)
       // what this thread wrote into the other stage comes before the copies into it
       fence_smem_to_async();
       __syncthreads();  // stage c has arrived, the other one is free, the state can be read
-      if (c + 1 < chunks && tid == 0) issue(c + 1);
+      if (c + 1 < chunks && tid == 0) {
+        issue_prep(c + 1);
+        issue_inputs(c + 1);
+      }
       if constexpr (kOut) {
         uint8_t* stage = smem + (c & 1) * St::kBytes;
         const uint32_t sg = sbase + (c & 1) * St::kBytes;
@@ -503,6 +515,8 @@ __global__ void __launch_bounds__(G * kStripThreads, 1)
 #pragma unroll
       for (int e = 0; e < 4; ++e) st[n][e] = 0.f;
   }
+  grid_dependency_wait();
+  allow_dependent_launch();
   for (int c = 0; c < chunks; ++c) {
     const uint32_t sbuf = ex + Ex::kS + (c & 1) * Ex::kState;
     put_state<KD>(sbuf, me.warp, lane, st);
@@ -601,8 +615,6 @@ __global__ void __launch_bounds__(kStripThreads, 1)
   const int h = blockIdx.y;
   const int hk = h / (a.Hv / a.Hk);
   const int v0 = blockIdx.x * 16, strip = blockIdx.x;
-  grid_dependency_wait();
-  allow_dependent_launch();
   const int b = seq_by_length(a.seq, blockIdx.z, lane);
   const long long start = seq_start(a.seq, b), end = seq_end(a.seq, b);
   const long long base = seq_base(a.seq, b);
@@ -625,27 +637,35 @@ __global__ void __launch_bounds__(kStripThreads, 1)
 
   if (side) {
     const int tid = threadIdx.x - kGroupThreads;
-    auto issue = [&](int c) {  // one thread
+    // one thread: the call's inputs, and what the kernels before have made of them
+    auto issue_inputs = [&](int c) {
       uint8_t* st = smem + (c & 1) * St::kBytes;
       uint64_t* bar = &full[c & 1];
       const int t0 = static_cast<int>(start + static_cast<long long>(c) * kChunk);
-      const long long hs = (base + c) * a.Hv + h;
       mbar_arrive_expect_tx(bar, 6 * kTriBytes + 784 + 3 * kStripBytes + 2 * St::kK + 2048);
-      const uint8_t* prep = a.prep + hs * kPrepBytes;
       tma_load_2d(st + St::kV, &maps.do_strip, h * a.V + v0, t0, bar);
-      bulk_copy_g2s(st + St::kTri, prep, 6 * kTriBytes, bar);
-      bulk_copy_g2s(st + St::kScal, prep + kPrepTri, 784, bar);
 #pragma unroll
       for (int kt = 0; kt < KD / 64; ++kt) {
         tma_load_2d(st + St::kK + kt * kTileBytes, &maps.k, hk * KD + kt * 64, t0, bar);
         tma_load_2d(st + St::kQ + kt * kTileBytes, &maps.q, hk * KD + kt * 64, t0, bar);
       }
+    };
+    auto issue_made = [&](int c) {
+      uint8_t* st = smem + (c & 1) * St::kBytes;
+      uint64_t* bar = &full[c & 1];
+      const long long hs = (base + c) * a.Hv + h;
+      const uint8_t* prep = a.prep + hs * kPrepBytes;
+      bulk_copy_g2s(st + St::kTri, prep, 6 * kTriBytes, bar);
+      bulk_copy_g2s(st + St::kScal, prep + kPrepTri, 784, bar);
       bulk_copy_g2s(st + St::kW, a.w_ws + (hs * (a.V / 16) + strip) * (3LL * kStripBytes),
                     3 * kStripBytes, bar);
     };
     bool alive = true;
     uint32_t phases = 0;  // a bit per stage
-    if (chunks > 0 && tid == 0) issue(chunks - 1);
+    if (chunks > 0 && tid == 0) issue_inputs(chunks - 1);
+    grid_dependency_wait();
+    allow_dependent_launch();
+    if (chunks > 0 && tid == 0) issue_made(chunks - 1);
     for (int c = chunks - 1; c >= 0; --c) {
       const long long left = end - start - static_cast<long long>(c) * kChunk;
       if ((tid < 32 || left < kChunk) && alive)
@@ -675,7 +695,10 @@ __global__ void __launch_bounds__(kStripThreads, 1)
         pbuf[i * 32] = make_float4(a.scale * t[i][0], a.scale * t[i][1], a.scale * t[i][2],
                                    a.scale * t[i][3]);
       bar_arrive(kBarA, kStripThreads);
-      if (c > 0 && tid == 0) issue(c - 1);
+      if (c > 0 && tid == 0) {
+        issue_inputs(c - 1);
+        issue_made(c - 1);
+      }
       // Q^T (scale gamma dO)
       get_strip(t, me.strip<1>(sg + St::kV, 0));
 #pragma unroll
@@ -752,6 +775,8 @@ __global__ void __launch_bounds__(kStripThreads, 1)
 #pragma unroll
       for (int e = 0; e < 4; ++e) d[n][e] = 0.f;
   }
+  grid_dependency_wait();
+  allow_dependent_launch();
   for (int c = chunks - 1; c >= 0; --c) {
     put_state<KD>(ex + Ex::kS, me.warp, lane, d);
     __syncthreads();
