@@ -25,6 +25,11 @@
 // shared-memory stages with bulk copies, the consumer warps own TPR threads per row and CPT
 // 16-byte chunks per thread, row blocks are assigned round-robin, so each input byte is read
 // from HBM once and the row sums between the passes cost shared-memory reads only.
+//
+// 16384 x 4096, BF16: forward 108 us (96% of the measured copy's rate), forward and backward 313
+// (the backward about 205, 81%): the backward's 45 instructions an element, two computing warps
+// a scheduler and two sums across eight warps a row.  512 threads with the same two chunks each
+// spill (486 us), with one chunk each wait on sixteen warps' barriers (364).
 #pragma once
 
 #include "device_common.cuh"

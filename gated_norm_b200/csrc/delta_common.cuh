@@ -87,12 +87,6 @@ __device__ __forceinline__ uint32_t addr_bt(uint32_t tile, int row0, int col0, i
 __device__ __forceinline__ uint32_t addr_a(uint32_t tile, int row0, int col0, int lane) {
   return tile + tile_off(row0 + (lane & 15), (col0 >> 3) + (lane >> 4));
 }
-// A operand of the transposed tile (transposing ldmatrix or stmatrix): m are columns
-// col0..+15, k are rows row0..+15.
-__device__ __forceinline__ uint32_t addr_at(uint32_t tile, int row0, int col0, int lane) {
-  return tile + tile_off(row0 + (lane & 7) + ((lane >> 4) << 3), (col0 >> 3) + ((lane >> 3) & 1));
-}
-
 __device__ __forceinline__ float bf_lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
@@ -115,15 +109,6 @@ __device__ __forceinline__ void split3(float x, float y, uint32_t p[3]) {
   p[1] = pack_bf16x2(r.x, r.y);
   r = left_of(r, p[1]);
   p[2] = pack_bf16x2(r.x, r.y);
-}
-
-// A fragments (hi, lo) of a 16 x 16 block from two accumulator tiles 16 x 8 side by side.
-__device__ __forceinline__ void split_frag(const float t0[4], const float t1[4], uint32_t hi[4],
-                                           uint32_t lo[4]) {
-  split2(t0[0], t0[1], hi[0], lo[0]);
-  split2(t0[2], t0[3], hi[1], lo[1]);
-  split2(t1[0], t1[1], hi[2], lo[2]);
-  split2(t1[2], t1[3], hi[3], lo[3]);
 }
 
 // 16-byte asynchronous copy, zero-filled where `live` is false (nothing is read then).
@@ -293,10 +278,4 @@ __device__ __forceinline__ void clear_rows(uint8_t* p, int bytes, int n, int til
     *reinterpret_cast<uint4*>(p + t * tile + r * bytes + x * 16) = make_uint4(0u, 0u, 0u, 0u);
   }
 }
-// Copies contiguous bytes (a multiple of 16).
-template <int kThreads>
-__device__ __forceinline__ void load_flat(uint32_t dst, const uint8_t* src, int bytes, int tid) {
-  for (int i = tid * 16; i < bytes; i += kThreads * 16) cp16(dst + i, src + i, true);
-}
-
 }  // namespace gnorm

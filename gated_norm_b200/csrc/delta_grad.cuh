@@ -28,7 +28,10 @@
 // The products of a chunk and head take about 5600 cycles of the tensor cores, what it reads
 // (S and D in FP32, W, dX, dO: 240 KB) as long again.  A CTA stays on its SM and goes through
 // its chunks; the next one's tiles are copied, its states brought to L2 and its scalars computed
-// behind the products of the current one.
+// behind the products of the current one.  8192 tokens x 16 heads of 128 x 128: 212 us, 28000
+// cycles a chunk and head (mma.sync, a CTA per chunk: 362 us); what is left are the phases that
+// follow one another -- S cut and stored, products, D cut and stored, products, pair terms,
+// products -- with one CTA's shared memory and all of tensor memory in use.
 #pragma once
 
 #include "delta_common.cuh"

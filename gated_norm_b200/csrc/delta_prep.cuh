@@ -10,7 +10,8 @@
 //
 //   R = Kb_pr - sum_{r<=q<p} Kb_pq (beta N_qr)    N_pr = R - N_pp (beta R)
 //
-// N_qr (times beta) and R live in the unused upper half of Kb.
+// N_qr (times beta) and R live in the unused upper half of Kb.  8192 tokens x 16 heads: 57 us
+// (row by row, 64 steps: 76), 65 MB written; bound by instructions, 0.40 a cycle and scheduler.
 #pragma once
 
 #include "delta_common.cuh"

@@ -7,7 +7,8 @@
 // Bound by HBM: the state is read and written once, 8 K V bytes a head against 2 (2 K + 2 V)
 // of everything else.  A CTA holds VT columns of one head's state in registers: float4 loads
 // of whole rows, all issued before the first use, a fixed-order sum over the row groups
-// through shared memory, stores straight from the registers.
+// through shared memory, stores straight from the registers.  256 rows x 32 heads of 128 x 128
+// (1.08 GB): 183 us, 5.9 TB/s, 91% of the measured copy; 4 rows x 16 heads: 6 us, the launch.
 #pragma once
 
 #include "delta_common.cuh"
