@@ -451,6 +451,66 @@ def test_autograd():
         close(v.grad, recurrence(y)["dv"], "dv")
 
 
+@pytest.mark.parametrize("V", [64, 128])
+def test_thousands_of_sequences(V):
+    """Sequences of 0 to 2 tokens: 3000 of them, as strips (V = 64) and as whole heads."""
+    lens = [(1, 2, 0, 1)[(i * 7) % 4] for i in range(3000)]
+    x = make(lens, 1, 1, 64, V, state=True, tail=3)
+    got = call(x)
+    n = sum(lens)
+    # by hand: a token's step from its sequence's state, all first tokens, then all second ones
+    cu = x["cu"].long()
+    S = x["S0"].double()[:, 0]
+    for i in range(2):
+        at = (cu[1:] - cu[:-1] > i).nonzero()[:, 0]
+        t = cu[at] + i
+        q, k, v = (x[m][t, 0].double() for m in ("q", "k", "v"))
+        R = x["g"][t, 0].double().exp()[:, None, None] * S[at]
+        u = x["beta"][t].double() * (v - (k[:, :, None] * R).sum(1))
+        R = R + k[:, :, None] * u[:, None, :]
+        o = x["scale"] * (q[:, :, None] * R).sum(1)
+        terms = x["scale"] * (q[:, :, None] * R).square().sum(1).sqrt()
+        close(got["o"][t, 0], o, "o", size={"o": terms})
+        S[at] = R
+    close(got["S"], S[:, None], "S")
+    assert not got["o"][n:].any()
+    empty = (cu[1:] == cu[:-1]).nonzero()[:, 0]
+    assert torch.equal(got["S"][empty], x["S0"][empty])
+    assert torch.equal(got["dS0"][empty], x["dS"][empty])
+
+
+def test_streams_and_workspaces_of_the_caller():
+    """An explicit stream for every call, one workspace for calls in a row on it, and outputs of
+    the caller's."""
+    x = make([100, 60], 1, 2, 128, 128, state=True)
+    want = call(x)
+    s = torch.cuda.Stream()
+    ws = torch.empty(gn.gnorm_delta_workspace_bytes(160, 2, 2, 128, 128, True), dtype=torch.uint8,
+                     device="cuda")
+    a = (x["q"], x["k"], x["v"], x["g"], x["beta"])
+    kw = dict(scale=x["scale"], cu_seqlens=x["cu"], initial_state=x["S0"], workspace_buf=ws, stream=s)
+    out = {n: torch.empty_like(want[n]) for n in GRADS}
+    o, S = torch.empty_like(x["v"]), torch.empty_like(x["S0"])
+    torch.cuda.synchronize()
+    for _ in range(2):
+        r = gn.gnorm_delta_fwd(*a, o=o, final_state=S, **kw)
+        assert r[0] is o and r[1].data_ptr() == S.data_ptr()
+        r = gn.gnorm_delta_bwd(x["do"], *a, dfinal_state=x["dS"],
+                               **{("dinitial_state" if n == "dS0" else n): t for n, t in out.items()}, **kw)
+    s.synchronize()
+    assert torch.equal(o, want["o"]) and torch.equal(S, want["S"])
+    for n in GRADS:
+        assert torch.equal(out[n], want[n]), n
+    y = step_case(3, 1, 2, 128, 128, 5)
+    ref = y["pool"].clone()
+    o1 = step(y, ref, slots=y["slots"])
+    pool = y["pool"].clone()
+    torch.cuda.synchronize()
+    o2 = step(y, pool, slots=y["slots"], stream=s)
+    s.synchronize()
+    assert torch.equal(o1, o2) and torch.equal(ref, pool)
+
+
 def test_first_call_of_a_thread():
     """A thread that has made no CUDA call yet: both directions run there."""
     import threading
