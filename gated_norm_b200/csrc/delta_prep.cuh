@@ -5,13 +5,12 @@
 // for each value head of the group the decays, and N by blocks of 16, in FP32.  Bound by the
 // dependent steps of the substitution, 64 if taken row by row, so only the diagonal blocks are
 // (a warp each, 16 steps: column j of N solves n_i = Kb_ij - sum_{l<i} Kb_il beta_l n_l, two
-// threads a column); the others follow as products, the 16 columns of a block column four to
-// each warp, so that no step waits for another warp:
+// threads a column); the others follow as products on the tensor cores, operands in three BF16
+// parts, a block column per warp, so that no step waits for another warp:
 //
-//   R = Kb_pr - sum_{r<=q<p} Kb_pq (beta N_qr)    N_pr = R - N_pp (beta R)
+//   R = Kb_pr - sum_{r<=q<p} (Kb_pq beta) N_qr    N_pr = R - N_pp (beta R)
 //
-// N_qr (times beta) and R live in the unused upper half of Kb.  8192 tokens x 16 heads: 57 us
-// (row by row, 64 steps: 76), 65 MB written; bound by instructions, 0.40 a cycle and scheduler.
+// N's parts are read where they go out, beta R passes through N_pr's place.
 #pragma once
 
 #include "delta_common.cuh"
@@ -153,17 +152,17 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(const __gri
       }
     }
     __syncthreads();
-    // the diagonal blocks, N in Kb's place; column tid / 2, this thread keeps beta_l n_l of the
+    // the diagonal blocks; column tid / 2, this thread keeps beta_l n_l of the
     // blocks of four rows l whose number has its parity
     {
       const int j = tid >> 1, par = tid & 1, jj = j - i0;
-      float* sub = kb + i0 * kKbLd + i0;
+      const float* sub = kb + i0 * kKbLd + i0;
       float x[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] = 0.f;
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        float* row = sub + i * kKbLd;
+        const float* row = sub + i * kKbLd;
         float s0 = 0.f, s1 = 0.f;
 #pragma unroll
         for (int m = 0; m < (i + 7) / 8; ++m) {
@@ -177,12 +176,10 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(const __gri
         s0 += __shfl_xor_sync(0xffffffffu, s0, 1);
         const float n = i > jj ? row[jj] - s0 : 0.f;
         if (((i >> 2) & 1) == par) x[(i >> 3) * 4 + (i & 3)] = scal[i0 + i] * n;
-        __syncwarp();  // the row has been read
         // this thread's parts: the first, or the second and third
         const __nv_bfloat16 p0 = __float2bfloat16_rn(n);
         uint8_t* dst = tiles + tri_off(i0 + i, j);
         if (par == 0) {
-          row[jj] = n;
           *reinterpret_cast<__nv_bfloat16*>(dst) = p0;
         } else {
           const float r1 = n - __bfloat162float(p0);
@@ -194,49 +191,102 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(const __gri
       }
     }
     __syncthreads();
-    // the blocks below: this lane has row lane / 2 of a block and two of its columns
+    // the blocks below, a warp per block column r
+    const uint32_t tri = sq;  // the parts in shared memory
+    // this lane's matrix row of the 16 x 16 block (p, r): the left operand's matrices in its order
+    // (rows first), the right one's and a product's own in theirs
+    auto left_at = [&](int p, int r) {
+      return tri + (tri_row(2 * p + ((lane >> 3) & 1)) + 2 * r + (lane >> 4)) * 128 + (lane & 7) * 16;
+    };
+    auto right_at = [&](int p, int r) { return left_at(p, r); };  // (transposing loads: k first)
     {
-      const int row = lane >> 1, jc = warp * 4 + (lane & 1) * 2;
-      // v -= A (16 x 16, rows of kb) B (its row k at b + k * kKbLd, times f[k] where given)
-      auto product = [&](float2& v, const float* A, const float* B, const float* f) {
+      const int r = warp, row = lane >> 2, col = 2 * (lane & 3);
+      for (int p = r + 1; p < 4; ++p) {
+        // accumulators: two tiles of eight columns, in FP32
+        float x[2][4], y[2][4];
+        const float* kp = kb + (p * 16 + row) * kKbLd + col;
 #pragma unroll
-        for (int k = 0; k < 16; k += 4) {
-          const float4 x = *reinterpret_cast<const float4*>(A + k);
-          const float xs[4] = {x.x, x.y, x.z, x.w};
+        for (int t = 0; t < 2; ++t) {
+          const float2 u = *reinterpret_cast<const float2*>(kp + r * 16 + t * 8);
+          const float2 v = *reinterpret_cast<const float2*>(kp + 8 * kKbLd + r * 16 + t * 8);
+          x[t][0] = u.x;
+          x[t][1] = u.y;
+          x[t][2] = v.x;
+          x[t][3] = v.y;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[t][e] = 0.f;
+        }
+        // x -= the products of A's parts and of a block's parts, the larger and the smaller ones
+        // in sums of their own
+        auto product = [&](const uint32_t (*A)[4], uint32_t at) {
+#pragma unroll
+          for (int n = 0; n < 3; ++n) {
+            uint32_t b[4];
+            ldsm4t(b, at + n * kTriBytes);
+#pragma unroll
+            for (int m = 0; m + n < 3; ++m) {
+              float(*acc)[4] = m + n == 0 ? x : y;
+              mma16816(acc[0], A[m], b[0], b[1]);
+              mma16816(acc[1], A[m], b[2], b[3]);
+            }
+          }
+        };
+        for (int q = r; q < p; ++q) {
+          // -Kb_pq diag(beta)
+          uint32_t A[3][4];
+          const float2 b0 = *reinterpret_cast<const float2*>(scal + q * 16 + col);
+          const float2 b1 = *reinterpret_cast<const float2*>(scal + q * 16 + 8 + col);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {  // rows 0 and 8, then columns 8 on
+            const float2 u = *reinterpret_cast<const float2*>(kp + (i & 1) * 8 * kKbLd + q * 16 + (i >> 1) * 8);
+            const float2 be = i < 2 ? b0 : b1;
+            uint32_t parts[3];
+            split3(-u.x * be.x, -u.y * be.y, parts);
+#pragma unroll
+            for (int m = 0; m < 3; ++m) A[m][i] = parts[m];
+          }
+          product(A, right_at(q, r));
+        }
+        // R times beta into its own place, then N_pr = R - N_pp (beta R)
+        auto put = [&](float f0, float f1) {
+          uint32_t f[3][4];
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            uint32_t u[3], v[3];
+            split3(f0 * x[t][0], f0 * x[t][1], u);
+            split3(f1 * x[t][2], f1 * x[t][3], v);
+#pragma unroll
+            for (int m = 0; m < 3; ++m) {
+              f[m][2 * t] = u[m];
+              f[m][2 * t + 1] = v[m];
+            }
+          }
+          __syncwarp();
+#pragma unroll
+          for (int m = 0; m < 3; ++m) stsm4(left_at(p, r) + m * kTriBytes, f[m]);
+          __syncwarp();
+        };
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float2 y = *reinterpret_cast<const float2*>(B + (k + e) * kKbLd);
-            const float c = f != nullptr ? xs[e] * f[k + e] : xs[e];
-            v.x = fmaf(-c, y.x, v.x);
-            v.y = fmaf(-c, y.y, v.y);
+            x[t][e] += y[t][e];
+            y[t][e] = 0.f;
           }
+        put(scal[p * 16 + row], scal[p * 16 + 8 + row]);
+        uint32_t A[3][4];
+#pragma unroll
+        for (int m = 0; m < 3; ++m) {
+          ldsm4(A[m], left_at(p, p) + m * kTriBytes);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) A[m][i] ^= 0x80008000u;
         }
-      };
+        product(A, right_at(p, r));
 #pragma unroll
-      for (int r = 0; r < 3; ++r) {
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int p = r + 1; p < 4; ++p) {
-          const float* krow = kb + (p * 16 + row) * kKbLd;  // this row of Kb_p.
-          float2 v = *reinterpret_cast<const float2*>(krow + r * 16 + jc);
-          product(v, krow + r * 16, kb + (r * 16) * kKbLd + r * 16 + jc, scal + r * 16);
-#pragma unroll
-          for (int q = r + 1; q < p; ++q)
-            product(v, krow + q * 16, kb + (r * 16) * kKbLd + q * 16 + jc, nullptr);
-          float* up = kb + (r * 16 + row) * kKbLd + p * 16 + jc;  // block (r, p)
-          const float be = scal[p * 16 + row];
-          *reinterpret_cast<float2*>(up) = make_float2(be * v.x, be * v.y);
-          __syncwarp();
-          product(v, krow + p * 16, kb + (r * 16) * kKbLd + p * 16 + jc, nullptr);
-          __syncwarp();
-          *reinterpret_cast<float2*>(up) = make_float2(be * v.x, be * v.y);
-          __syncwarp();
-          uint32_t parts[3];
-          split3(v.x, v.y, parts);
-#pragma unroll
-          for (int e = 0; e < 3; ++e)
-            *reinterpret_cast<uint32_t*>(tiles + e * kTriBytes + tri_off(p * 16 + row, r * 16 + jc)) =
-                parts[e];
-        }
+          for (int e = 0; e < 4; ++e) x[t][e] += y[t][e];
+        put(1.f, 1.f);
       }
     }
     __syncthreads();
