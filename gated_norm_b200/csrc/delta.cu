@@ -307,6 +307,7 @@ int gnorm_delta_fwd(const gnorm_delta_fwd_desc* desc, void* stream) {
   DeviceInfo info;
   if ((st = device_info(&info)) != GNORM_OK) return st;
   a.err = info.err_word;
+  a.sms = info.num_sms;
   const cudaStream_t s = as_stream(stream);
   const bool whole = whole_heads(a, info.num_sms);
   const int groups = scan_groups(a, info.num_sms);
@@ -385,6 +386,7 @@ int gnorm_delta_bwd(const gnorm_delta_bwd_desc* desc, void* stream) {
   DeviceInfo info;
   if ((st = device_info(&info)) != GNORM_OK) return st;
   a.err = info.err_word;
+  a.sms = info.num_sms;
   a.slots = delta_slots(d.T, d.B);
   const cudaStream_t s = as_stream(stream);
   const int groups = scan_groups(a, info.num_sms);

@@ -228,6 +228,7 @@ struct DeltaArgs {
   long long lddq = 0, lddk = 0, lddv = 0, lddg = 0, lddbeta = 0;
   unsigned* err = nullptr;  // the device error word
   long long slots = 0;
+  int sms = 1;  // of the device
   // rows behind the last sequence that are to be zeroed
   int n_zero = 0;
   uint8_t* zero_p[5] = {};

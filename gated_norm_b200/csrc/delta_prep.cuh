@@ -3,10 +3,9 @@
 //
 // One CTA per (chunk, key head): K K^T and Q K^T once (BF16 operands, exact, FP32 sums), then
 // for each value head of the group the decays, and N by blocks of 16, in FP32.  Bound by the
-// dependent steps of the substitution, 64 if taken row by row, so only the diagonal blocks are
-// (a warp each, 16 steps: column j of N solves n_i = Kb_ij - sum_{l<i} Kb_il beta_l n_l, two
-// threads a column); the others follow as products on the tensor cores, operands in three BF16
-// parts, a block column per warp, so that no step waits for another warp:
+// dependent steps of the substitution, 64 if taken row by row, so only blocks of 8 on the diagonal
+// are (column j of N solves n_i = Kb_ij - sum_{l<i} Kb_il beta_l n_l); the others follow as products on the tensor cores, operands in three BF16
+// parts, one distance from the diagonal after another:
 //
 //   R = Kb_pr - sum_{r<=q<p} (Kb_pq beta) N_qr    N_pr = R - N_pp (beta R)
 //
@@ -56,15 +55,30 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(const __gri
           *reinterpret_cast<uint16_t*>(a.zero_p[z] + (t0 + r) * a.zero_ld[z] + i) = 0;
     return;
   }
+  // The four warps' shares of the work below differ (the lower rows have more columns); CTAs that
+  // share an SM, a multiple of its number apart, give them to different schedulers.
+  const int rot = static_cast<int>((static_cast<unsigned>(slot) + gridDim.x * hk) / static_cast<unsigned>(a.sms));
+  const int wr = (warp + rot) & 3;
+  const int group = a.Hv / a.Hk;
+  // g and beta of two tokens a lane, for the warp that sums them, a head ahead
+  float4 gb = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto load_g = [&](int h) {
+    const int ta = 2 * lane, tb = ta + 1;
+    gb.x = ta < live ? clamp_decay(a.g[(t0 + ta) * a.ldg + h]) : 0.f;
+    gb.y = tb < live ? clamp_decay(a.g[(t0 + tb) * a.ldg + h]) : 0.f;
+    gb.z = ta < live ? load_beta(a, t0 + ta, h) : 0.f;
+    gb.w = tb < live ? load_beta(a, t0 + tb, h) : 0.f;
+  };
   const uint32_t sq = smem_u32(smem), sk = sq + kTiles * kTileBytes;
   load_rows<kPrepThreads>(sq, a.q + t0 * a.ldq + static_cast<long long>(hk) * KD, a.ldq, KD, live, tid);
   load_rows<kPrepThreads>(sk, a.k + t0 * a.ldk + static_cast<long long>(hk) * KD, a.ldk, KD, live, tid);
   cp_commit();
+  if (wr == 0) load_g(hk * group);
   cp_wait<0>();
   __syncthreads();
 
-  // rows 16 warp .. +15 of K K^T and Q K^T, columns up to the diagonal block
-  const int i0 = warp * 16;
+  // rows 16 wr .. +15 of K K^T and Q K^T, columns up to the diagonal block
+  const int i0 = wr * 16;
   float kk[8][4], qk[8][4];
 #pragma unroll
   for (int n = 0; n < 8; ++n)
@@ -79,7 +93,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(const __gri
     ldsm4(aq, addr_a(sq + toff, i0, c0, lane));
 #pragma unroll
     for (int nb = 0; nb < 4; ++nb) {
-      if (nb <= warp) {
+      if (nb <= wr) {
         uint32_t bk[4];
         ldsm4(bk, addr_b(sk + toff, nb * 16, c0, lane));
         mma16816(kk[2 * nb], ak, bk[0], bk[1]);
@@ -91,27 +105,26 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(const __gri
   }
   __syncthreads();  // the q and k tiles are free
 
-  const int group = a.Hv / a.Hk;
   uint8_t* tiles = smem;  // N in three parts, P in three parts
   for (int r = 0; r < group; ++r) {
     const int h = hk * group + r;
-    if (warp == 0) {
+    if (wr == 0) {
       // running sum of g in FP64: differences of far terms stay exact to FP32
       const int ta = 2 * lane, tb = ta + 1;
-      const float ga = ta < live ? clamp_decay(a.g[(t0 + ta) * a.ldg + h]) : 0.f;
-      const float gb = tb < live ? clamp_decay(a.g[(t0 + tb) * a.ldg + h]) : 0.f;
-      double s = static_cast<double>(ga) + static_cast<double>(gb);
+      const float4 cur = gb;
+      if (r + 1 < group) load_g(h + 1);
+      double s = static_cast<double>(cur.x) + static_cast<double>(cur.y);
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
         const double o = __shfl_up_sync(0xffffffffu, s, off);
         if (lane >= off) s += o;
       }
       const double total = __shfl_sync(0xffffffffu, s, 31);
-      const double Ga = s - static_cast<double>(gb);
+      const double Ga = s - static_cast<double>(cur.y);
       Gs[ta] = decay_sum(Ga);
       Gs[tb] = decay_sum(s);
-      scal[ta] = ta < live ? load_beta(a, t0 + ta, h) : 0.f;
-      scal[tb] = tb < live ? load_beta(a, t0 + tb, h) : 0.f;
+      scal[ta] = cur.z;
+      scal[tb] = cur.w;
       scal[64 + ta] = expf(static_cast<float>(Ga));
       scal[64 + tb] = expf(static_cast<float>(s));
       scal[128 + ta] = expf(static_cast<float>(total - Ga));
@@ -124,7 +137,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(const __gri
     const float2 Ga = Gs[ra], Gb = Gs[rb];
 #pragma unroll
     for (int n = 0; n < 8; ++n) {
-      if (n > 2 * warp + 1) break;  // above the diagonal block: nothing is read there
+      if (n > 2 * wr + 1) break;  // above the diagonal block: nothing is read there
       const int c = n * 8 + 2 * (lane & 3);
       const float2 G0 = Gs[c], G1 = Gs[c + 1];
       float d[4] = {0.f, 0.f, 0.f, 0.f};
@@ -152,46 +165,67 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(const __gri
       }
     }
     __syncthreads();
-    // the diagonal blocks; column tid / 2, this thread keeps beta_l n_l of the
-    // blocks of four rows l whose number has its parity
+    // The diagonal blocks, a warp each: its two 8 x 8 blocks by substitution, a column per lane
+    // (lanes 16..31 repeat it), then the block below them by two products in FP32.
     {
-      const int j = tid >> 1, par = tid & 1, jj = j - i0;
-      const float* sub = kb + i0 * kKbLd + i0;
-      float x[8];
+      const float* beta = scal + i0;
+      float* blk = kb + i0 * kKbLd + i0;
+      {
+        const int at = ((lane >> 3) & 1) * 8, j = lane & 7;
+        float* sub = blk + at * kKbLd + at;
+        float n[8], x[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = 0.f;
+        for (int i = 0; i < 8; ++i) {
+          const float4 c0 = *reinterpret_cast<const float4*>(sub + i * kKbLd);
+          const float4 c1 = *reinterpret_cast<const float4*>(sub + i * kKbLd + 4);
+          const float c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+          float s = i > j ? sub[i * kKbLd + j] : 0.f;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float* row = sub + i * kKbLd;
-        float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-        for (int m = 0; m < (i + 7) / 8; ++m) {
-          const float4 cf = *reinterpret_cast<const float4*>(row + (2 * m + par) * 4);
-          s0 = fmaf(cf.x, x[4 * m], s0);
-          s1 = fmaf(cf.y, x[4 * m + 1], s1);
-          s0 = fmaf(cf.z, x[4 * m + 2], s0);
-          s1 = fmaf(cf.w, x[4 * m + 3], s1);
+          for (int l = 0; l < i; ++l) s = fmaf(-c[l], x[l], s);
+          n[i] = i > j ? s : 0.f;
+          x[i] = beta[at + i] * n[i];
         }
-        s0 += s1;
-        s0 += __shfl_xor_sync(0xffffffffu, s0, 1);
-        const float n = i > jj ? row[jj] - s0 : 0.f;
-        if (((i >> 2) & 1) == par) x[(i >> 3) * 4 + (i & 3)] = scal[i0 + i] * n;
-        // this thread's parts: the first, or the second and third
-        const __nv_bfloat16 p0 = __float2bfloat16_rn(n);
-        uint8_t* dst = tiles + tri_off(i0 + i, j);
-        if (par == 0) {
-          *reinterpret_cast<__nv_bfloat16*>(dst) = p0;
-        } else {
-          const float r1 = n - __bfloat162float(p0);
-          const __nv_bfloat16 p1 = __float2bfloat16_rn(r1);
-          *reinterpret_cast<__nv_bfloat16*>(dst + kTriBytes) = p1;
-          *reinterpret_cast<__nv_bfloat16*>(dst + 2 * kTriBytes) =
-              __float2bfloat16_rn(r1 - __bfloat162float(p1));
+        __syncwarp();
+        if (lane < 16) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sub[i * kKbLd + j] = n[i];
         }
+        __syncwarp();
       }
+      const int row = lane >> 2, c = 2 * (lane & 3);
+      float* low = blk + (8 + row) * kKbLd;  // this row of the lower blocks
+      float2 v = *reinterpret_cast<const float2*>(low + c);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float m = low[k] * beta[k];
+        const float2 y = *reinterpret_cast<const float2*>(blk + k * kKbLd + c);
+        v.x = fmaf(-m, y.x, v.x);
+        v.y = fmaf(-m, y.y, v.y);
+      }
+      float* up = blk + row * kKbLd + 8 + c;  // the upper right block is free
+      *reinterpret_cast<float2*>(up) = make_float2(beta[8 + row] * v.x, beta[8 + row] * v.y);
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float m = low[8 + k];
+        const float2 y = *reinterpret_cast<const float2*>(blk + k * kKbLd + 8 + c);
+        v.x = fmaf(-m, y.x, v.x);
+        v.y = fmaf(-m, y.y, v.y);
+      }
+      auto put = [&](int i, int j, float2 u) {
+        uint32_t parts[3];
+        split3(u.x, u.y, parts);
+#pragma unroll
+        for (int m = 0; m < 3; ++m)
+          *reinterpret_cast<uint32_t*>(tiles + m * kTriBytes + tri_off(i0 + i, i0 + j)) = parts[m];
+      };
+      put(row, c, *reinterpret_cast<const float2*>(blk + row * kKbLd + c));
+      put(row, 8 + c, make_float2(0.f, 0.f));
+      put(8 + row, c, v);
+      put(8 + row, 8 + c, *reinterpret_cast<const float2*>(low + 8 + c));
     }
     __syncthreads();
-    // the blocks below, a warp per block column r
+    // the blocks below, one distance from the diagonal after another
     const uint32_t tri = sq;  // the parts in shared memory
     // this lane's matrix row of the 16 x 16 block (p, r): the left operand's matrices in its order
     // (rows first), the right one's and a product's own in theirs
@@ -200,8 +234,12 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(const __gri
     };
     auto right_at = [&](int p, int r) { return left_at(p, r); };  // (transposing loads: k first)
     {
-      const int r = warp, row = lane >> 2, col = 2 * (lane & 3);
-      for (int p = r + 1; p < 4; ++p) {
+      const int row = lane >> 2, col = 2 * (lane & 3);
+      for (int d = 1; d < 4; ++d) {
+        // three blocks, two, one: to the warps that have fewer columns above
+        const int r = d == 1 ? wr : d == 2 ? 2 - wr : -wr, p = r + d;
+        if (d > 1) __syncthreads();
+        if (r < 0 || p > 3) continue;
         // accumulators: two tiles of eight columns, in FP32
         float x[2][4], y[2][4];
         const float* kp = kb + (p * 16 + row) * kKbLd + col;
