@@ -1,4 +1,5 @@
 // delta.cu -- launchers and extern "C" entry points of the gated delta rule.
+#include "delta_cols.cuh"
 #include "delta_grad.cuh"
 #include "delta_head.cuh"
 #include "delta_prep.cuh"
@@ -76,7 +77,8 @@ cudaError_t launch_prep(const DeltaArgs& a, cudaStream_t s) {
 }
 
 // Strips of 16 columns a CTA.  One while they all fit on the SMs side by side, so that every
-// strip has an SM's four schedulers to itself; otherwise two, which share the right operands.
+// strip has an SM's four schedulers to itself; otherwise two, which share the right operands
+// (where the forward has no better way: run_fwd).
 int scan_groups(const DeltaArgs& a, int num_sms) {
   return static_cast<long long>(a.V / 16) * a.Hv * a.seq.B <= num_sms ? 1 : 2;
 }
@@ -104,18 +106,19 @@ cudaError_t launch_grad(const DeltaArgs& a, const DeltaMaps& m, int num_sms, cud
   return launch_grid(delta_grad_kernel<KD, VD>, grid, kGradThreads, GradSmem<KD, VD>::kBytes, s, a, m);
 }
 
-// A whole head per CTA instead of strips?  Strips need about 2850 cycles each a chunk on an SM
-// that is full of them (22800 a head of 128 columns), a whole head 7000, whose chunks follow one
-// another on one SM.  Sequences of one length (the host knows): once two heads share five SMs
-// (16384 tokens x 64 heads 1565 us against 1872; 8 x 1024 tokens x 16 heads 148 against 254; 32
-// heads of 16384 tokens 1400 against 955).  Packed sequences, of which the longest decides and
-// is often twice the mean: with more heads than SMs (8 sequences of 16384 tokens in all x 32
-// heads 582 against 889; 8 of 8192 x 16: 274 against 252).  Heads of 64 columns waste half of
-// an instruction's rows (8 of 8192 x 32, K = V = 64: 275 against 246).
+// A whole head per CTA instead of strips or columns?  An SM takes about 4.1 us a chunk for a
+// whole head, 2.6 for a quarter (delta_cols.cuh).  Sequences of one length (the host knows): once
+// quarters do not fit the SMs side by side (one of 4096 tokens: 40 heads 310 us against
+// 395, 64 heads 336 against 416; 32 heads, before the last steps, 354 against 212; 8 x 1024
+// tokens x 16 heads 114 against 222).
+// Packed sequences, of which the longest decides and is often twice the mean: with more heads
+// than SMs (5 of 4096 tokens in all x 32 heads 150 against 237; 5 of 2048 x 16, of nearly equal
+// lengths, 71 against 75; 8 of 8192 x 16, less even, 274 against 252).  Heads of
+// 64 columns waste half of an instruction's rows (8 of 8192 x 32, K = V = 64: 275 against 246).
 bool whole_heads(const DeltaArgs& a, int num_sms) {
   const long long heads = static_cast<long long>(a.seq.B) * a.Hv;
   if (a.V != 128) return false;
-  return a.seq.cu != nullptr && a.seq.B > 1 ? heads > num_sms : 5 * heads > 2LL * num_sms;
+  return a.seq.cu != nullptr && a.seq.B > 1 ? heads > num_sms : 4 * heads > num_sms;
 }
 
 template <int KD>
@@ -124,13 +127,24 @@ cudaError_t launch_head_fwd(const DeltaArgs& a, const DeltaMaps& m, cudaStream_t
   return launch_grid(delta_head_fwd_kernel<KD, 128>, grid, kHeadThreads, head_smem<KD, 128>(), s, a, m);
 }
 
+cudaError_t launch_cols_fwd(const DeltaArgs& a, const DeltaMaps& m, cudaStream_t s) {
+  const dim3 grid(static_cast<unsigned>(a.V / ColsSmem::VT), static_cast<unsigned>(a.Hv),
+                  static_cast<unsigned>(a.seq.B));
+  return launch_grid(delta_cols_fwd_kernel, grid, ColsSmem::kThreads, ColsSmem::kBytes, s, a, m);
+}
+
 template <int KD>
 cudaError_t run_fwd(const DeltaArgs& a, const DeltaMaps& m, bool whole, int groups, cudaStream_t s) {
   const cudaError_t e = launch_prep<KD>(a, s);
   if (e != cudaSuccess) return e;
   if (whole) return launch_head_fwd<KD>(a, m, s);
-  return groups == 1 ? launch_scan_fwd<KD, 1, true, false>(a, m, s)
-                     : launch_scan_fwd<KD, 2, true, false>(a, m, s);
+  if (groups == 1) return launch_scan_fwd<KD, 1, true, false>(a, m, s);
+  // two strips of K = 64 on an SM beat their columns on tcgen05 (4096 tokens x 32 heads of K = 64,
+  // V = 128: 186 us against 202), of K = 128 they do not (235 against 210)
+  if constexpr (KD == 128)
+    return launch_cols_fwd(a, m, s);
+  else
+    return launch_scan_fwd<KD, 2, true, false>(a, m, s);
 }
 
 template <int KD>

@@ -194,6 +194,7 @@ constexpr int kTriBytes = 40 * 128;  // tri_row(8) matrices
 __device__ __forceinline__ uint32_t tri_off(int i, int j) {  // element (i, j)
   return static_cast<uint32_t>((tri_row(i >> 3) + (j >> 3)) * 128 + (i & 7) * 16 + (j & 7) * 2);
 }
+constexpr int kTriGrid = 8192;  // a part in an 8 x 8 grid of matrices, an operand of tcgen05
 constexpr long long kPrepTri = 6LL * kTriBytes;
 constexpr long long kPrepScal = 1024;
 constexpr long long kPrepBytes = kPrepTri + kPrepScal;

@@ -42,7 +42,6 @@ namespace gnorm {
 
 constexpr int kGradThreads = 512;
 constexpr int kMLd = 65;
-constexpr unsigned kErrWaitMma = 8u;  // a wait for the tensor cores ran out
 
 template <int KD, int VD>
 struct GradSmem {

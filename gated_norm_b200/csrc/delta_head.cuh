@@ -12,9 +12,9 @@
 //   3  U = (lambda Y) K                   4  O = gamma O + Y P^T,  S' = e^{G_C} S + U
 //
 // Eight warps own the rows (a thread one column of V: half of S's row in FP32 registers for the
-// whole sequence, half of the chunk's tokens), one thread issues the products, one warp the
-// copies.  A chunk takes about 7000 cycles (X 1600, its rows 900, D 1350, Y 1050, U 850 with the
-// output's product behind it, S 1150): half of it in the products' latency, which another head
+// whole sequence, half of the chunk's tokens), one warp issues the products, one the copies.  A
+// chunk takes about 4.1 us (40 heads of 4096 tokens 310 us; 367 while one thread issued the
+// products from a branch of its own), half of it in the products' latency, which another head
 // on the SM could fill if tensor memory (480 of 512 columns here) had the room.
 #pragma once
 
@@ -25,7 +25,6 @@ namespace gnorm {
 
 constexpr int kHeadWarps = 8;
 constexpr int kHeadThreads = (kHeadWarps + 2) * 32;
-constexpr int kGridBytes = 8192;  // a part of N or P: 8 x 8 matrices in an 8 x 8 grid
 
 template <int KD, int VD>
 struct HeadStage {
@@ -33,7 +32,7 @@ struct HeadStage {
   static constexpr int kK = KD / 64 * kTileBytes;
   static constexpr int kV = 2 * kK;
   static constexpr int kTri = kV + VD / 64 * kTileBytes;  // N (three parts), P (two)
-  static constexpr int kScal = kTri + 5 * kGridBytes;
+  static constexpr int kScal = kTri + 5 * kTriGrid;
   static constexpr int kBytes = kScal + 1024;
 };
 template <int KD, int VD>
@@ -87,8 +86,8 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
     fence_barrier_init();
   }
   // N and P above the diagonal, where no copy arrives
-  for (int i = tid; i < 2 * 5 * kGridBytes / 16; i += kHeadThreads) {
-    uint8_t* p = smem + (i >= 5 * kGridBytes / 16 ? St::kBytes - 5 * kGridBytes : 0) + St::kTri + i * 16;
+  for (int i = tid; i < 2 * 5 * kTriGrid / 16; i += kHeadThreads) {
+    uint8_t* p = smem + (i >= 5 * kTriGrid / 16 ? St::kBytes - 5 * kTriGrid : 0) + St::kTri + i * 16;
     *reinterpret_cast<uint4*>(p) = make_uint4(0u, 0u, 0u, 0u);
   }
   fence_smem_to_async();
@@ -102,7 +101,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
   tc_fence_after();
   grid_dependency_wait();  // (the kernel before is this call's own: see delta_scan.cuh)
   allow_dependent_launch();
-  const uint32_t tmem = *tslot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tslot, 0);
   bool alive = true;
   auto wait = [&](uint64_t* bar, uint32_t parity, unsigned bit) {
     if (alive) alive = mbar_spin(bar, parity & 1u, a.err, bit);
@@ -137,7 +136,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
       // a row of matrices each: five parts of eight rows
       for (int i = lane; i < 40; i += 32) {
         const int part = i >> 3, t = i & 7;
-        bulk_copy_g2s(st + St::kTri + part * kGridBytes + t * 1024,
+        bulk_copy_g2s(st + St::kTri + part * kTriGrid + t * 1024,
                       prep + part * kTriBytes + tri_row(t) * 128, (t / 2 + 1) * 256, bar);
       }
       if (c + 1 == chunks && last_live < kChunk) {
@@ -150,7 +149,8 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
     }
   } else if (warp == kHeadWarps) {
     // ---- products
-    if (lane == 0) {
+    {
+      const bool lead = elect_one();
       constexpr uint32_t idK = mma_desc<false, false, 64>(), idU = mma_desc<false, true, KD>();
       for (int c = 0; c < chunks; ++c) {
         const uint32_t sg = sbase + (c & 1) * St::kBytes;
@@ -161,20 +161,20 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
         const uint64_t kt = smem_desc(sg + St::kK, kTileBytes, 1024);  // transposed
         const uint64_t td = smem_desc_plain(sg + St::kTri, 128, 1024);
         auto rows_at = [](int ks) { return static_cast<uint32_t>((ks >> 2) * kTileBytes + (ks & 3) * 32); };
-        auto tri_at = [](int part, int kb) { return static_cast<uint32_t>(part * kGridBytes + 2 * kb * 128); };
+        auto tri_at = [](int part, int kb) { return static_cast<uint32_t>(part * kTriGrid + 2 * kb * 128); };
 #pragma unroll
         for (int part = 0; part < 3; ++part)
 #pragma unroll
           for (int ks = 0; ks < KD / 16; ++ks)
-            tc_mma_t(tmem + kX, tmem + kS + part * kHalf + ks * 8, desc_at(kd, rows_at(ks)), idK, part + ks > 0);
-        tc_commit(x_out);
+            tc_mma_tw(lead, tmem + kX, tmem + kS + part * kHalf + ks * 8, desc_at(kd, rows_at(ks)), idK, part + ks > 0);
+        if (lead) tc_commit(x_out);
         if (c > 0) wait(o_free, c - 1, kErrWaitMma);
         tc_fence_after();
 #pragma unroll
         for (int part = 0; part < 2; ++part)
 #pragma unroll
           for (int ks = 0; ks < KD / 16; ++ks)
-            tc_mma_t(tmem + kO, tmem + kS + part * kHalf + ks * 8, desc_at(qd, rows_at(ks)), idK, part + ks > 0);
+            tc_mma_tw(lead, tmem + kO, tmem + kS + part * kHalf + ks * 8, desc_at(qd, rows_at(ks)), idK, part + ks > 0);
         wait(a_in, c, kErrWaitMma);
         tc_fence_after();
 #pragma unroll
@@ -183,27 +183,27 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
           for (int x = 0; x < 3; ++x)
 #pragma unroll
             for (int n = 0; n + x < 3; ++n)
-              tc_mma_t(tmem + kX, tmem + kA + x * 32 + kb * 8, desc_at(td, tri_at(n, kb)), idK, kb + x + n > 0);
-        tc_commit(d_out);
+              tc_mma_tw(lead, tmem + kX, tmem + kA + x * 32 + kb * 8, desc_at(td, tri_at(n, kb)), idK, kb + x + n > 0);
+        if (lead) tc_commit(d_out);
         wait(y_in, c, kErrWaitMma);
         tc_fence_after();
 #pragma unroll
         for (int part = 0; part < 3; ++part)
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
-            tc_mma_t(tmem + kX, tmem + kS + part * 32 + ks * 8,
+            tc_mma_tw(lead, tmem + kX, tmem + kS + part * 32 + ks * 8,
                      desc_at(kt, ks * 2048), idU, part + ks > 0);
-        tc_commit(u_out);
+        if (lead) tc_commit(u_out);
         wait(o_in, c, kErrWaitMma);
         tc_fence_after();
 #pragma unroll
         for (int kb = 0; kb < 4; ++kb) {
-          tc_mma_t(tmem + kO, tmem + kA + kb * 8, desc_at(td, tri_at(3, kb)), idK, true);
-          tc_mma_t(tmem + kO, tmem + kA + 32 + kb * 8, desc_at(td, tri_at(3, kb)), idK, true);
-          tc_mma_t(tmem + kO, tmem + kA + kb * 8, desc_at(td, tri_at(4, kb)), idK, true);
+          tc_mma_tw(lead, tmem + kO, tmem + kA + kb * 8, desc_at(td, tri_at(3, kb)), idK, true);
+          tc_mma_tw(lead, tmem + kO, tmem + kA + 32 + kb * 8, desc_at(td, tri_at(3, kb)), idK, true);
+          tc_mma_tw(lead, tmem + kO, tmem + kA + kb * 8, desc_at(td, tri_at(4, kb)), idK, true);
         }
-        tc_commit(o_out);
-        tc_commit(&empty[c & 1]);
+        if (lead) tc_commit(o_out);
+        if (lead) tc_commit(&empty[c & 1]);
       }
       // the last chunk's products end before tensor memory is freed: o_out is waited for below
     }

@@ -22,7 +22,8 @@
 // The tensor cores of the fifth generation take at least 64 rows an instruction: a head's 128
 // columns would be one tile on one SM, its 66000 values a chunk would be cut and scaled by
 // that SM alone, and the other SMs would wait -- the heads of a layer are fewer than the SMs.
-// (delta_head.cuh does that, for batches with more heads than SMs.)
+// (delta_head.cuh does that, for batches of many heads; delta_cols.cuh gives 32 columns an SM
+// with the tokens as rows, for the forward of heads too many for a strip an SM.)
 //
 // A chunk of 128 x 128 heads takes, with a strip per SM, 2800 cycles without the output and 3400
 // with it (S K 690, X 195, N 740, Y 285, the update 690, the state's parts 150), the backward's

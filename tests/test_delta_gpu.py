@@ -250,6 +250,91 @@ def test_whole_heads_reset_and_repeat():
     close(S, ref["S"], "S")
 
 
+def quarters(seqs, Hv, V, packed):
+    """Heads of K = 128 that have 32 columns per CTA: more strips of 16 than SMs, and too few whole
+    heads."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert V // 16 * Hv * seqs > sms and Hv * seqs * (1 if packed or V == 64 else 4) <= sms
+    return Hv
+
+
+@pytest.mark.parametrize("T", [1, 2, 63, 64, 65, 129, 200])
+def test_quarters_of_one_sequence(T):
+    Hv = quarters(1, 24, 128, False)
+    check(make([T], 8, Hv, 128, 128, state=T % 2 == 1, seed=T,
+               beta=torch.bfloat16 if T % 3 else torch.float32))
+
+
+@pytest.mark.parametrize("V", [64, 128])
+def test_quarters_packed(V):
+    lens = [65, 0, 130, 64, 1]
+    Hv = quarters(len(lens), 8, V, True)
+    x = make(lens, 2, Hv, 128, V, state=True, tail=70, seed=V)
+    check(x)
+    first = call(x)
+    for n in ("q", "k", "v", "g", "beta"):
+        x[n][260:] = float("nan")  # behind the last sequence
+    x["v"][100, 1] = float("nan")  # in one sequence, one head
+    x["S0"][3, 2, 5, 7] = float("inf")
+    got = call(x)
+    keep = list(range(65)) + [259]
+    assert torch.equal(got["o"][keep], first["o"][keep])
+    assert torch.equal(got["S"][[0, 1, 4]], first["S"][[0, 1, 4]])
+    others = [0] + list(range(3, Hv))
+    assert torch.equal(got["o"][:260, others], first["o"][:260, others])
+    assert torch.equal(got["S"][:, others], first["S"][:, others])
+    assert not bool(torch.isfinite(got["S"][2, 1]).all())
+
+
+def test_quarters_reset_and_repeat():
+    Hv = quarters(1, 20, 128, False)
+    x = make([200], 1, Hv, 128, 128, state=True, decay=0.01)
+    x["k"] = x["k"][:1].expand(200, 1, 128).contiguous()
+    x["beta"][:] = 0.9
+    x["g"][30] = float("-inf")
+    x["g"][130] = torch.finfo(torch.float32).min
+    o, S = gn.gnorm_delta_fwd(x["q"], x["k"], x["v"], x["g"], x["beta"], scale=x["scale"],
+                              cu_seqlens=x["cu"], initial_state=x["S0"], output_final_state=True)
+    ref = recurrence(dict(x, g=x["g"].clamp(min=-700.0)), grads=False)
+    close(o, ref["o"], "o", size=ref["size"])
+    close(S, ref["S"], "S")
+
+
+def test_quarters_streams_slices_and_replay():
+    """Strided inputs and output, two streams at once, captured and replayed; what lies between
+    the output's rows and behind the sequence stays."""
+    T, Hv = 150, quarters(1, 24, 128, False)
+    x = make([T], 8, Hv, 128, 128, state=True)
+    args = lambda v: (x["q"], x["k"], v, x["g"], x["beta"])
+    kw = dict(scale=x["scale"], initial_state=x["S0"], output_final_state=True)
+    o, S = gn.gnorm_delta_fwd(*args(x["v"]), **kw)
+    wide = torch.full((T, Hv * 128 + 16), 5.0, dtype=torch.bfloat16, device="cuda")
+    wide[:, 8:8 + Hv * 128] = x["v"].reshape(T, -1)
+    v = wide[:, 8:8 + Hv * 128].unflatten(1, (Hv, 128))
+    cu = torch.tensor([0, 140], dtype=torch.int32, device="cuda")
+    place = torch.full_like(wide, 7.0)
+    o2, S2 = gn.gnorm_delta_fwd(*args(v), **kw, o=place[:, 8:8 + Hv * 128].unflatten(1, (Hv, 128)))
+    assert torch.equal(o2, o) and torch.equal(S2, S)
+    assert bool((place[:, :8] == 7.0).all()) and bool((place[:, 8 + Hv * 128:] == 7.0).all())
+    part = torch.full_like(x["v"], 7.0)
+    gn.gnorm_delta_fwd(*args(x["v"]), **kw, cu_seqlens=cu, o=part)
+    assert torch.equal(part[:140], o[:140]) and bool((part[140:] == 7.0).all())
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        o3, S3 = gn.gnorm_delta_fwd(*args(v), **kw)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            o4, S4 = gn.gnorm_delta_fwd(*args(v), **kw)
+    o5, S5 = gn.gnorm_delta_fwd(*args(x["v"]), **kw)
+    torch.cuda.current_stream().wait_stream(s)
+    g.replay()
+    torch.cuda.synchronize()
+    for a, b in ((o3, S3), (o4, S4), (o5, S5)):
+        assert torch.equal(a, o) and torch.equal(b, S)
+    assert gn.gnorm_device_error(reset=True) == 0
+
+
 def test_many_heads_of_one_key_head():
     check(make([97], 1, 8, 128, 128))
 
