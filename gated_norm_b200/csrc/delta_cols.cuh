@@ -157,6 +157,9 @@ __global__ void __launch_bounds__(ColsSmem::kThreads, 1)
         if (lane == 0) mbar_arrive(cleared);
       }
     }
+    // the last arrivals from the tensor cores come before the CTA leaves
+    for (int c = chunks; c < chunks + 2; ++c)
+      if (c >= 2) wait(&empty[c & 1], static_cast<uint32_t>((c >> 1) - 1), kErrWaitEmpty);
   } else if (warp == kRowWarps + 2) {
     // ---- products on the way from state to state
     constexpr uint32_t id3 = mma_desc<false, true, 3 * VT>(), idU = mma_desc<true, true, 3 * VT>();

@@ -147,6 +147,9 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
         if (lane == 0) mbar_arrive(cleared);
       }
     }
+    // the last arrivals from the tensor cores come before the CTA leaves
+    for (int c = chunks; c < chunks + 2; ++c)
+      if (c >= 2) wait(&empty[c & 1], static_cast<uint32_t>((c >> 1) - 1), kErrWaitEmpty);
   } else if (warp == kHeadWarps) {
     // ---- products
     {
