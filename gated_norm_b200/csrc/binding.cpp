@@ -42,6 +42,15 @@ void check_type(const Tensor& t, const char* name, int types) {
 }
 int type_of(const Tensor& t) { return t.scalar_type() == at::kFloat ? kFp32 : kBf16; }
 
+// A stride of more than one row, token or slot, as a descriptor takes it.  There 0 means "packed",
+// while a tensor's 0 (`expand`) means one row in the place of all: never passed on.
+int64_t distance(int64_t stride, const char* name, const char* what) {
+  if (stride == 0)
+    bad_value(std::string(name) + ": its " + what + " share memory (an expanded tensor); pass " + name +
+              ".contiguous()");
+  return stride;
+}
+
 void* ptr(const Tensor& t) { return t.numel() ? t.data_ptr() : nullptr; }
 void* ptr(const OptTensor& t) { return t ? ptr(*t) : nullptr; }
 
@@ -79,7 +88,6 @@ Tensor scratch(const OptTensor& given, size_t need, const at::Device& dev) {
 // column stride.
 int64_t rows(const Tensor& t, const char* name, int types, const Tensor* like) {
   check_type(t, name, types);
-  if (!t.is_cuda()) bad_value(std::string(name) + " must be a CUDA tensor");
   if (like != nullptr) {
     if (t.sizes() != like->sizes())
       bad_value("a " + shape_of(*like) + " and " + name + " " + shape_of(t) + " differ");
@@ -87,9 +95,14 @@ int64_t rows(const Tensor& t, const char* name, int types, const Tensor* like) {
   } else if (t.dim() < 1) {
     bad_value(std::string(name) + " must have a last dimension N");
   }
-  if (t.is_contiguous()) return t.size(-1);
-  if (t.dim() == 2 && t.stride(1) == 1) return t.size(0) > 1 ? t.stride(0) : t.size(1);
-  bad_value(std::string(name) + ": rows need unit column stride (2-D row-strided views or contiguous tensors)");
+  int64_t ld = t.size(-1);
+  if (!t.is_contiguous()) {
+    if (t.dim() != 2 || t.stride(1) != 1)
+      bad_value(std::string(name) + ": rows need unit column stride (2-D row-strided views or contiguous tensors)");
+    if (t.size(0) > 1) ld = distance(t.stride(0), name, "rows");
+  }
+  if (!t.is_cuda()) bad_value(std::string(name) + " must be a CUDA tensor");
+  return ld;
 }
 
 void vec(const Tensor& t, int64_t n, int types, const char* name, const at::Device& dev) {
@@ -204,9 +217,6 @@ std::tuple<int, Tensor, Tensor, OptTensor, Tensor, Tensor, OptTensor> block_bwd(
 int64_t tokens(const Tensor& t, const char* name, at::IntArrayRef lead, at::IntArrayRef tail, int types,
                const at::Device& dev) {
   check_type(t, name, types);
-  if (!t.is_cuda()) bad_value(std::string(name) + " must be a CUDA tensor");
-  if (t.device() != dev)
-    bad_value(std::string(name) + " is on " + t.device().str() + ", the other tensors on " + dev.str());
   const int64_t n = static_cast<int64_t>(lead.size()), m = static_cast<int64_t>(tail.size());
   bool same = t.dim() == n + m;
   for (int64_t i = 0; same && i < n + m; ++i) same = t.size(i) == (i < n ? lead[i] : tail[i - n]);
@@ -216,19 +226,23 @@ int64_t tokens(const Tensor& t, const char* name, at::IntArrayRef lead, at::IntA
       want += (i ? ", " : "") + std::to_string(i < n ? lead[i] : tail[i - n]);
     bad_value(std::string(name) + " must be (" + want + "), got " + shape_of(t));
   }
-  int64_t width = 1;
-  for (int64_t x : tail) width *= x;
-  if (t.is_contiguous() || t.numel() == 0) return width;
-  int64_t want = 1;
-  for (int64_t i = n + m - 1; i >= n; --i) {
-    if (t.size(i) > 1 && t.stride(i) != want)
-      bad_value(std::string(name) + ": the heads of a token must be packed");
-    want *= t.size(i);
+  int64_t ld = 1;  // packed: the values of a token
+  for (int64_t x : tail) ld *= x;
+  if (!t.is_contiguous() && t.numel() != 0) {
+    int64_t want = 1;
+    for (int64_t i = n + m - 1; i >= n; --i) {
+      if (t.size(i) > 1 && t.stride(i) != want)
+        bad_value(std::string(name) + ": the heads of a token must be packed");
+      want *= t.size(i);
+    }
+    const int64_t inner = n == 2 && lead[1] > 1 ? 1 : 0;  // the dimension of neighbouring tokens
+    if (lead[inner] > 1) ld = distance(t.stride(inner), name, "tokens");
+    if (n == 2 && lead[0] > 1 && t.stride(0) != ld * lead[1])
+      bad_value(std::string(name) + ": tokens must be evenly spaced over the batch");
   }
-  if (n == 1) return lead[0] > 1 ? t.stride(0) : width;
-  const int64_t ld = lead[1] > 1 ? t.stride(1) : lead[0] > 1 ? t.stride(0) : width;
-  if (lead[0] > 1 && t.stride(0) != ld * lead[1])
-    bad_value(std::string(name) + ": tokens must be evenly spaced over the batch");
+  if (!t.is_cuda()) bad_value(std::string(name) + " must be a CUDA tensor");
+  if (t.device() != dev)
+    bad_value(std::string(name) + " is on " + t.device().str() + ", the other tensors on " + dev.str());
   return ld;
 }
 
@@ -398,6 +412,8 @@ std::tuple<int, Tensor> delta_step(const Tensor& q, const Tensor& k, const Tenso
     bad_value("state must be [pool, " + std::to_string(d.Hv) + ", " + std::to_string(d.K) + ", " +
               std::to_string(d.V) + "] on " + dev.str() + " with packed slots, got " + shape_of(state) +
               " on " + state.device().str());
+  d.pool = state.size(0);
+  d.ldstate = d.pool > 1 ? distance(state.stride(0), "state", "slots") : want;
   if (slots) {
     if (slots->scalar_type() != at::kInt) bad_type("slots", "int32", *slots);
     if (slots->sizes() != lead || !slots->is_contiguous() || slots->device() != dev)
@@ -414,8 +430,6 @@ std::tuple<int, Tensor> delta_step(const Tensor& q, const Tensor& k, const Tenso
   d.beta_fp32 = type_of(beta) == kFp32;
   d.scale = static_cast<float>(scale ? *scale : 1.0 / std::sqrt(static_cast<double>(d.K)));
   d.state = static_cast<float*>(ptr(state));
-  d.pool = state.size(0);
-  d.ldstate = d.pool > 1 ? state.stride(0) : want;
   d.slots = static_cast<const int*>(ptr(slots));
   d.o = ptr(o);
   return {gnorm_delta_step(&d, here.stream), o};

@@ -150,16 +150,20 @@ def _mat(t: torch.Tensor, name: str):
         raise ValueError(f"{name} must have a last dimension N")
     if t.dtype != torch.bfloat16:
         raise TypeError(f"{name} must be bfloat16, got {t.dtype}")
+    N = ld = t.shape[-1]
+    M = t.numel() // N if N else 0
+    if not t.is_contiguous():
+        if t.dim() != 2 or t.stride(1) != 1:
+            raise ValueError(f"{name}: rows need unit column stride (2-D row-strided views or "
+                             "contiguous tensors)")
+        if M > 1:
+            ld = t.stride(0)
+            if ld == 0:  # the library takes 0 as "packed"
+                raise ValueError(f"{name}: its rows share memory (an expanded tensor); pass "
+                                 f"{name}.contiguous()")
     if t.device.type != "cuda":
         raise ValueError(f"{name} must be a CUDA tensor")
-    N = t.shape[-1]
-    if t.is_contiguous():
-        return (t.numel() // N if N else 0), N, N
-    if t.dim() == 2 and t.stride(1) == 1:
-        M = t.shape[0]
-        return M, N, (t.stride(0) if M > 1 else N)
-    raise ValueError(f"{name}: rows need unit column stride (2-D row-strided views or "
-                     "contiguous tensors)")
+    return M, N, ld
 
 
 def _same(a: torch.Tensor, b: torch.Tensor, an: str, bn: str):
