@@ -43,22 +43,21 @@ inline Region mat(const void* p, int64_t rows, int64_t cols, int64_t ld, int ele
 
 inline int64_t floor_div(int64_t a, int64_t b) { return a / b - ((a % b != 0) && ((a < 0) != (b < 0))); }
 
-// Exact for two matrices with the same stride and width (their elements interleave
-// row by row); whole-extent overlap otherwise.
+// Exact for two matrices with the same stride in bytes, of any widths (columns of one wider
+// buffer, which interleave row by row); whole-extent overlap otherwise.
 inline bool overlaps(const Region& a, const Region& b) {
   if (a.p == nullptr || b.p == nullptr || a.bytes == 0 || b.bytes == 0) return false;
   const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), a1 = a0 + a.bytes;
   const uintptr_t b0 = reinterpret_cast<uintptr_t>(b.p), b1 = b0 + b.bytes;
   if (!(a0 < b1 && b0 < a1)) return false;
-  if (!(a.is_mat && b.is_mat && a.ld == b.ld && a.cols == b.cols &&
-        a.elem == b.elem)) return true;
-  const int64_t diff = static_cast<int64_t>(b0 - a0);  // two's complement difference
-  if (diff % a.elem != 0) return true;
-  const int64_t d = diff / a.elem, L = a.ld, n = a.cols;
+  const int64_t L = a.ld * a.elem, na = a.cols * a.elem, nb = b.cols * b.elem;
+  // rows of at most a stride each: a row of b meets one or two rows of a
+  if (!(a.is_mat && b.is_mat && L == b.ld * b.elem && na <= L && nb <= L)) return true;
+  const int64_t d = static_cast<int64_t>(b0 - a0);  // two's complement difference
   const int64_t q = floor_div(d, L), delta = d - q * L;  // b's row j starts in a's row q + j
   auto rows_meet = [&](int64_t off) { return off < a.rows && off + b.rows > 0; };
-  if (delta < n && rows_meet(q)) return true;          // columns [delta, n) of the same row
-  if (delta + n > L && rows_meet(q + 1)) return true;  // b's row runs into a's next row
+  if (delta < na && rows_meet(q)) return true;          // b's row starts inside that row
+  if (delta + nb > L && rows_meet(q + 1)) return true;  // or runs into a's next row
   return false;
 }
 
