@@ -9,6 +9,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/extension.h>
 
+#include <initializer_list>
 #include <optional>
 #include <string>
 #include <tuple>
@@ -133,6 +134,14 @@ void block_common(Desc& d, const Tensor& a, const Tensor& r, const OptTensor& g,
   d.alpha = static_cast<const float*>(ptr(alpha));
 }
 
+// Tells autograd that a call has written tensors of the caller's: one that a graph has saved before
+// must not go into its backward as if it were the old one.  (An inference tensor is in no graph.)
+void wrote(int status, std::initializer_list<const OptTensor*> given) {
+  if (status != GNORM_OK) return;
+  for (const OptTensor* t : given)
+    if (*t && !(*t)->is_inference()) (*t)->unsafeGetTensorImpl()->bump_version();
+}
+
 Tensor out_like(const OptTensor& t, const Tensor& like, at::ScalarType type) {
   return t ? *t : at::empty(like.sizes(), like.options().dtype(type));
 }
@@ -158,7 +167,9 @@ std::tuple<int, Tensor, Tensor, Tensor, Tensor> block_fwd(
   d.z = ptr(z);
   d.rstd1 = static_cast<float*>(ptr(rstd1));
   d.rstd2 = static_cast<float*>(ptr(rstd2));
-  return {gnorm_block_fwd(&d, here.stream), h, z, rstd1, rstd2};
+  const int st = gnorm_block_fwd(&d, here.stream);
+  wrote(st, {&h_, &z_, &rstd1_, &rstd2_});
+  return {st, h, z, rstd1, rstd2};
 }
 
 std::tuple<int, Tensor, Tensor, OptTensor, Tensor, Tensor, OptTensor> block_bwd(
@@ -207,7 +218,9 @@ std::tuple<int, Tensor, Tensor, OptTensor, Tensor, Tensor, OptTensor> block_bwd(
   d.dalpha = static_cast<float*>(ptr(dalpha));
   d.workspace = ptr(ws);
   d.workspace_bytes = ws.nbytes();
-  return {gnorm_block_bwd(&d, here.stream), da, dr, dg, dw1, dw2, dalpha};
+  const int st = gnorm_block_bwd(&d, here.stream);
+  wrote(st, {&da_, &dr_, &dg_, &dw1_, &dw2_, &dalpha_});
+  return {st, da, dr, dg, dw1, dw2, dalpha};
 }
 
 // ------------------------------------------------------------------------- delta rule
@@ -335,7 +348,9 @@ std::tuple<int, Tensor, OptTensor> delta_fwd(
   f.zero_tail = !o_ && cu;
   f.workspace = ptr(ws);
   f.workspace_bytes = ws.nbytes();
-  return {gnorm_delta_fwd(&f, here.stream), o, final_state};
+  const int st = gnorm_delta_fwd(&f, here.stream);
+  wrote(st, {&o_, &final_});
+  return {st, o, final_state};
 }
 
 std::tuple<int, Tensor, Tensor, Tensor, Tensor, Tensor, OptTensor> delta_bwd(
@@ -378,7 +393,9 @@ std::tuple<int, Tensor, Tensor, Tensor, Tensor, Tensor, OptTensor> delta_bwd(
   b.zero_tail = cu && given == 0;
   b.workspace = ptr(ws);
   b.workspace_bytes = ws.nbytes();
-  return {gnorm_delta_bwd(&b, here.stream), dq, dk, dv, dg, dbeta, dinitial};
+  const int st = gnorm_delta_bwd(&b, here.stream);
+  wrote(st, {&dq_, &dk_, &dv_, &dg_, &dbeta_, &dinitial_});
+  return {st, dq, dk, dv, dg, dbeta, dinitial};
 }
 
 std::tuple<int, Tensor> delta_step(const Tensor& q, const Tensor& k, const Tensor& v, const Tensor& g,
@@ -432,7 +449,10 @@ std::tuple<int, Tensor> delta_step(const Tensor& q, const Tensor& k, const Tenso
   d.state = static_cast<float*>(ptr(state));
   d.slots = static_cast<const int*>(ptr(slots));
   d.o = ptr(o);
-  return {gnorm_delta_step(&d, here.stream), o};
+  const int st = gnorm_delta_step(&d, here.stream);
+  const OptTensor pool = state;
+  wrote(st, {&pool, &o_});
+  return {st, o};
 }
 
 }  // namespace
