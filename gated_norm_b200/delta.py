@@ -108,13 +108,15 @@ class GatedDeltaNorm(torch.nn.Module):
         self.eps = eps
 
     def forward(self, q, k, v, g, beta, gate, *, scale=None, cu_seqlens=None, initial_state=None):
-        """(y, final_state) over whole sequences; gate: BF16, v's shape."""
+        """(y, final_state) over whole sequences; gate: BF16, v's shape (a slice of a wider
+        projection is copied: the norm's rows are all one distance apart).  The norm takes every
+        row, so gate has to be finite behind the last sequence too."""
         o, final = gated_delta_rule(q, k, v, g, beta, scale=scale, cu_seqlens=cu_seqlens,
                                     initial_state=initial_state)
-        return gated_rmsnorm(o, gate, self.weight, self.eps), final
+        return gated_rmsnorm(o, gate.contiguous(), self.weight, self.eps), final
 
     def step(self, q, k, v, g, beta, gate, state, *, slots=None, scale=None):
         """y for one token of each sequence; ``state`` is updated in place (no gradients)."""
         with torch.no_grad():
             o = gnorm_delta_step(q, k, v, g, beta, state, slots=slots, scale=scale)
-            return gated_rmsnorm(o, gate, self.weight, self.eps)
+            return gated_rmsnorm(o, gate.contiguous(), self.weight, self.eps)
