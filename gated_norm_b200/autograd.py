@@ -14,6 +14,13 @@ from .gnorm import gnorm_bwd, gnorm_fwd
 __all__ = ["GatedRMSNormFunction", "gated_rmsnorm", "GatedRMSNorm"]
 
 
+def _grad(t):
+    """An incoming gradient as the kernels take it: packed and 16-byte aligned.  One that autograd
+    cuts out of a flat buffer (the backward of a concatenation) starts anywhere."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 class GatedRMSNormFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, g, w, eps: float, deterministic: bool):
@@ -25,8 +32,7 @@ class GatedRMSNormFunction(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dy):
         x, g, w, rstd = ctx.saved_tensors
-        dy = dy.contiguous() if not dy.is_contiguous() else dy
-        dx, dg, dw = gnorm_bwd(dy, x, g, w, rstd, dw_fp32=w.dtype == torch.float32,
+        dx, dg, dw = gnorm_bwd(_grad(dy), x, g, w, rstd, dw_fp32=w.dtype == torch.float32,
                                deterministic=ctx.deterministic)
         return dx, dg, dw, None, None
 

@@ -10,6 +10,7 @@ import torch
 
 from . import _marshal
 from ._lib import lib
+from .autograd import _grad
 from .gnorm import _check, _handle
 
 __all__ = ["gnorm_block_fwd", "gnorm_block_bwd", "gnorm_block_bwd_workspace_bytes",
@@ -58,9 +59,9 @@ class BlockRMSNormFunction(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dh, dz):
         a, r, g, w1, w2, alpha, rstd1, rstd2 = ctx.saved_tensors
-        dh = None if dh is None else dh.contiguous()
+        dh = None if dh is None else _grad(dh)
         dz = torch.zeros(a.shape, dtype=a.dtype, device=a.device) if dz is None \
-            else dz.contiguous()
+            else _grad(dz)
         da, dr, dg, dw1, dw2, dalpha = gnorm_block_bwd(
             dh, dz, a, r, w1, w2, rstd1, rstd2, g=g, alpha=alpha,
             dw_fp32=w1.dtype == torch.float32)

@@ -9,7 +9,7 @@ import torch
 
 from . import _marshal
 from ._lib import lib
-from .autograd import gated_rmsnorm
+from .autograd import _grad, gated_rmsnorm
 from .gnorm import _check, _handle
 
 __all__ = ["gnorm_delta_fwd", "gnorm_delta_bwd", "gnorm_delta_step",
@@ -84,8 +84,8 @@ class GatedDeltaRuleFunction(torch.autograd.Function):
     def backward(ctx, do, dfinal):
         q, k, v, g, beta, initial_state, cu_seqlens = ctx.saved_tensors
         do = torch.zeros(v.shape, dtype=v.dtype, device=v.device) if do is None \
-            else do.contiguous()
-        dfinal = None if dfinal is None else dfinal.contiguous()
+            else _grad(do)
+        dfinal = None if dfinal is None else _grad(dfinal)
         dq, dk, dv, dg, dbeta, ds = gnorm_delta_bwd(
             do, q, k, v, g, beta, scale=ctx.scale, cu_seqlens=cu_seqlens,
             initial_state=initial_state, dfinal_state=dfinal)
