@@ -201,22 +201,30 @@ _ws_lock = threading.Lock()
 _ws_cache: dict = {}
 
 
-def workspace(M: int, N: int, deterministic: bool, device) -> torch.Tensor:
-    """A zero-initialised backward workspace for `device`, cached and grown as needed.
+def workspace(M: int, N: int, deterministic: bool, device, stream=None) -> torch.Tensor:
+    """A backward workspace for calls on `stream` of `device` (None = torch's current one), its
+    header zero, cached and grown as needed.
 
-    The cache holds one buffer per device; calls that may run concurrently (other streams)
-    must pass workspaces of their own.
+    The cache holds one buffer per device and stream, so calls that may run at once do not share
+    one.  A call that is being captured gets a buffer that the graph owns and clears itself: a
+    cached one would be in use by eager calls while the graph replays, and its memory another's
+    once the cache has grown.
     """
     device = torch.device(device)
     idx = device.index if device.index is not None else torch.cuda.current_device()
-    with torch.cuda.device(idx):
+    with torch.cuda.device(idx), torch.cuda.stream(stream):  # None: no change
         need = max(gnorm_bwd_workspace_bytes(M, N, deterministic), 256)
-    with _ws_lock:
-        buf = _ws_cache.get(idx)
-        if buf is None or buf.numel() < need:
-            buf = torch.zeros(need, dtype=torch.uint8, device=torch.device("cuda", idx))
-            _ws_cache[idx] = buf
-        return buf
+        if torch.cuda.is_current_stream_capturing():
+            buf = torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", idx))
+            buf[:256].zero_()
+            return buf
+        key = idx, _stream(None, torch.device("cuda", idx))
+        with _ws_lock:
+            buf = _ws_cache.get(key)
+            if buf is None or buf.numel() < need:
+                buf = torch.zeros(need, dtype=torch.uint8, device=torch.device("cuda", idx))
+                _ws_cache[key] = buf
+            return buf
 
 
 _host_cache: dict = {}
@@ -257,7 +265,7 @@ def _fwd_desc(x, g, w, eps, y, rstd):
     return d, y, rstd
 
 
-def _bwd_desc(dy, x, g, w, rstd, dx, dg, dw, dw_fp32, deterministic, ws):
+def _bwd_desc(dy, x, g, w, rstd, dx, dg, dw, dw_fp32, deterministic, ws, stream):
     M, N, ldx = _mat(x, "x")
     _, _, lddy = _mat(dy, "dy")
     _, _, ldg = _mat(g, "g")
@@ -280,7 +288,7 @@ def _bwd_desc(dy, x, g, w, rstd, dx, dg, dw, dw_fp32, deterministic, ws):
     else:
         _vec(dw, N, (dw_dtype,), "dw", x.device)
     if ws is None:
-        ws = workspace(M, N, deterministic, x.device)
+        ws = workspace(M, N, deterministic, x.device, stream)
     else:
         _device_buffer(ws, "workspace_buf", x.device)
     d = GnormBwdDesc(dy=_ptr(dy), lddy=lddy, x=_ptr(x), ldx=ldx, g=_ptr(g), ldg=ldg, w=_ptr(w),
@@ -308,7 +316,7 @@ def gnorm_bwd(dy, x, g, w, rstd, *, dx=None, dg=None, dw=None, dw_fp32: bool = F
     """Backward: returns (dx, dg, dw).  dw is FP32 if dw_fp32 else BF16.  Row-strided 2-D
     views are accepted for dy, x, g, dx, dg; w may be BF16 or FP32."""
     d, dx, dg, dw = _bwd_desc(dy, x, g, w, rstd, dx, dg, dw, dw_fp32, deterministic,
-                              workspace_buf)
+                              workspace_buf, stream)
     if rstd is None:
         raise ValueError("rstd is required")
     with _on(x.device):
@@ -323,7 +331,7 @@ def gnorm_ckpt_step(x, g, w, eps: float, dy, *, y=None, rstd=None, dx=None, dg=N
     """Checkpointed step (forward, forward again, backward): returns (y, rstd, dx, dg, dw)."""
     fd, y, rstd = _fwd_desc(x, g, w, eps, y, rstd)
     bd, dx, dg, dw = _bwd_desc(dy, x, g, w, rstd, dx, dg, dw, dw_fp32, deterministic,
-                               workspace_buf)
+                               workspace_buf, stream)
     with _on(x.device):
         st = lib.gnorm_ckpt_step_ex(ctypes.byref(fd), ctypes.byref(bd),
                                     _stream(stream, x.device))
@@ -338,7 +346,7 @@ def gnorm_fwd_bwd(x, g, w, eps: float, dy, *, y=None, rstd=None, dx=None, dg=Non
     checkpointed layer and its backward): returns (y, rstd, dx, dg, dw)."""
     fd, y, rstd = _fwd_desc(x, g, w, eps, y, rstd)
     bd, dx, dg, dw = _bwd_desc(dy, x, g, w, rstd, dx, dg, dw, dw_fp32, deterministic,
-                               workspace_buf)
+                               workspace_buf, stream)
     with _on(x.device):
         st = lib.gnorm_fwd_bwd_ex(ctypes.byref(fd), ctypes.byref(bd), _stream(stream, x.device))
     _check(st, "gnorm_fwd_bwd")
