@@ -179,7 +179,7 @@ DeltaLayout delta_layout(int64_t T, int64_t B, int64_t Hv, int64_t K, int64_t V,
     l.s = take(static_cast<size_t>(K * V) * 4);
     l.d = take(static_cast<size_t>(K * V) * 4);
     l.w = take(static_cast<size_t>(3 * V / 64) * kTileBytes);
-    l.x = take(static_cast<size_t>(V / 64) * kTileBytes);
+    l.x = take(static_cast<size_t>(2 * V / 64) * kTileBytes);
     l.dots = take(static_cast<size_t>(V / 16) * 128 * 4);
   }
   l.total = at;

@@ -23,7 +23,8 @@
 // weight is 2^-24 or more.  Three parts hold all 24 bits of an FP32 value, and with FP32 sums
 // the chunked form is as exact as FP32 arithmetic.  Two parts (16 to 17 bits) are not enough
 // for a state: where the terms of a sum take each other back (one key repeated), it was 4e-4
-// off.  Two parts remain where a product only reaches a BF16 output (o, dq, dk).
+// off.  Two parts remain where a product only reaches a BF16 output (o, dq, dk), whose half step of
+// 2^-8 is 100 times what they leave out.
 #pragma once
 
 #include "device_common.cuh"
@@ -219,7 +220,7 @@ struct DeltaArgs {
   uint8_t* s_ws = nullptr;  // [slots, Hv]: S before the chunk, FP32, in fragment order
   uint8_t* d_ws = nullptr;  // [slots, Hv]: the gradient of S after the chunk, likewise
   uint8_t* w_ws = nullptr;  // [slots, Hv, V/16]: W's strips (delta_scan.cuh)
-  uint8_t* x_ws = nullptr;  // [slots, Hv]: lo tiles of dX (dv holds hi)
+  uint8_t* x_ws = nullptr;  // [slots, Hv]: tiles of dX's second and third parts (dv holds the first)
   float* dots = nullptr;    // [slots, Hv, V/16, 2, 64]: each strip's share of b and dbeta
   const float* dstate_out = nullptr;
   float* dstate_in = nullptr;

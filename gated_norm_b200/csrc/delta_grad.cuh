@@ -21,18 +21,25 @@
 // rows; the 64 of a query-side product and the 64 of the key-side product with the same right
 // operand are one: [dO; dX] S^T, [dO; dX] W^T, [Q; K] K^T, [Ph; -Eh] K.  Rows 0..63 of every
 // accumulator belong to dQ, rows 64..127 to dK, and where only the key side has a product
-// (W D^T, the transposed Ph and Eh, the second parts of dX and W) the upper rows multiply
+// (W D^T, the transposed Ph and Eh, the further parts of dX) the upper rows multiply
 // whatever tile lies before it and are not read.  A thread owns one row and a quarter of the columns.
-// Operands that are not exact in BF16 are in two parts here: dq and dk are BF16.
+// dg is FP32, so what it comes from, the products with S and F and E, has S, W and dX in three parts
+// (24 bits; in two dg was 2e-6 to 3e-6 off, now 4e-7 to 5e-7).  What reaches only dq and dk, which
+// are BF16, is in two: D, Ph, Eh and W against D.
 //
-// The products of a chunk and head take about 5600 cycles of the tensor cores, what it reads
-// (S and D in FP32, W, dX, dO: 240 KB) as long again.  A CTA stays on its SM and goes through
-// its chunks; the next one's tiles are copied, its states brought to L2 and its scalars computed
-// behind the products of the current one.  8192 tokens x 16 heads of 128 x 128: 212 us, 28000
-// cycles a chunk and head (mma.sync, a CTA per chunk: 362 us); what is left are the phases that
-// follow one another -- S cut and stored, products, D cut and stored, products, pair terms,
-// products -- with one CTA's shared memory and all of tensor memory in use.
+// The products of a chunk and head take about 8000 cycles of the tensor cores, what it reads
+// (S and D in FP32, W, dX, dO, q, k: 300 KB) as long again.  A CTA stays on its SM and goes through
+// its chunks; the next one's tiles are copied, its states, q and k brought to L2 and its scalars
+// computed behind the products of the current one.  8192 tokens x 16 heads of 128 x 128: 248 us,
+// 33000 cycles a chunk and head (211 with two parts); what is left are the phases that follow one
+// another -- S cut and stored, products, D cut and stored, products, pair terms, products -- with
+// one CTA's shared memory and all of tensor memory in use.  S's third part has the place of q and
+// k until its product is done.  Its product first, and q and k copied and multiplied behind the
+// other ones, was slower (forward and backward 1073 us for 1066: the products are issued at the
+// tensor cores' pace and what follows them waits for q.k too).
 #pragma once
+
+#include <type_traits>
 
 #include "delta_common.cuh"
 #include "delta_scan.cuh"
@@ -40,18 +47,29 @@
 
 namespace gnorm {
 
+// Brings the box of a tile at these coordinates to L2.
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int c0, int c1) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(c0), "r"(c1)
+               : "memory");
+}
+
 constexpr int kGradThreads = 512;
 constexpr int kMLd = 65;
 
 template <int KD, int VD>
 struct GradSmem {
-  // [q][k] of each 64 columns of K, twice; then [do][dX hi][dX lo][W hi][W lo] of each 64
-  // columns of V
+  // S's third part; then [q][k] of each 64 columns of K
   static constexpr int kQK = 0;
   static constexpr int kQKBytes = KD / 64 * 2 * kTileBytes;
-  static constexpr int kA = 2 * kQKBytes;
-  // S, then D (hi and lo tiles); then Ph, -Eh (hi, then lo) and the pair terms' running sums;
-  // then dq and dk on their way out
+  // the third parts of W and dX: [W][dX] of each 64 columns of V; then [do] and the first two:
+  // [dX hi][dX lo][W hi][W lo]
+  static constexpr int kA3 = kQK + kQKBytes;
+  static constexpr int kA = kA3 + VD / 64 * 2 * kTileBytes;
+  static_assert(VD / 64 * (KD / 64) * kTileBytes <= kQKBytes, "S's third part");
+  // S's first two parts, then D (hi and lo tiles); then Ph, -Eh (hi, then lo) and the pair terms'
+  // running sums; then dq and dk on their way out
   static constexpr int kBig = kA + VD / 64 * 5 * kTileBytes;
   static constexpr int kState = 2 * (VD / 64) * (KD / 64) * kTileBytes;
   static constexpr int kPairs = 4 * kTileBytes + 128 * kMLd * 4;
@@ -59,7 +77,7 @@ struct GradSmem {
   // per item, twice: decay sums [64], beta, gamma, lambda, e^{G_C}, b and dbeta sums
   static constexpr int kItem = 512 + 1024 + 512;
   static constexpr int kWork = kScal + 2 * kItem;  // sums within an item
-  static constexpr int kBytes = kWork + (3 * 512 + 16) * 4 + 80 + 1024;  // 1024: alignment
+  static constexpr int kBytes = kWork + (3 * 512 + 16) * 4 + 88 + 1024;  // 1024: alignment
 };
 
 // What a CTA works on: a chunk and key head with live tokens, and one of its value heads.
@@ -94,7 +112,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
   float* red = rowsum + 512;                                        // [16]
   uint64_t* bar = reinterpret_cast<uint64_t*>(red + 16);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 1);
-  uint64_t* full = bar + 2;
+  uint64_t *full = bar + 2, *qk_full = bar + 3, *kk_done = bar + 10;
   GradItem* next = reinterpret_cast<GradItem*>(bar + 4);
 
   const int group = a.Hv / a.Hk;
@@ -130,39 +148,44 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
   // two neighbouring column tiles of a strip per warp and step
   auto pair_off = [&](int i) { return ((warp + i * (kGradThreads / 32)) * 2) * 32 + lane; };
   // one thread's copies, and every thread's pieces of W
-  auto load_tiles = [&](const GradItem& it, int qk_buf) {
+  auto load_tiles = [&](const GradItem& it) {
     const int h = it.hk * group + it.r;
     const long long hs = it.slot * a.Hv + h;
     const int t0 = static_cast<int>(it.t0);
     uint8_t* base = smem + L::kA;
     if (tid == 0) {
-      mbar_arrive_expect_tx(full, (3 * kVT + (it.r == 0 ? 2 * kKT : 0)) * kTileBytes);
+      const uint8_t* x = a.x_ws + hs * 2 * kVT * kTileBytes;
+      mbar_arrive_expect_tx(full, 4 * kVT * kTileBytes);
 #pragma unroll
       for (int vt = 0; vt < kVT; ++vt) {
         uint8_t* at = base + vt * 5 * kTileBytes;
         tma_load_2d(at, &maps.do_tile, h * VD + vt * 64, t0, full);
         tma_load_2d(at + kTileBytes, &maps.dv, h * VD + vt * 64, t0, full);
-        bulk_copy_g2s(at + 2 * kTileBytes, a.x_ws + (hs * kVT + vt) * kTileBytes, kTileBytes, full);
-      }
-      if (it.r == 0) {
-        uint8_t* qk = smem + L::kQK + qk_buf * L::kQKBytes;
-#pragma unroll
-        for (int kt = 0; kt < kKT; ++kt) {
-          tma_load_2d(qk + kt * 2 * kTileBytes, &maps.q, it.hk * KD + kt * 64, t0, full);
-          tma_load_2d(qk + (kt * 2 + 1) * kTileBytes, &maps.k, it.hk * KD + kt * 64, t0, full);
-        }
+        bulk_copy_g2s(at + 2 * kTileBytes, x + vt * kTileBytes, kTileBytes, full);
+        bulk_copy_g2s(smem + L::kA3 + (2 * vt + 1) * kTileBytes, x + (kVT + vt) * kTileBytes, kTileBytes, full);
       }
     }
 #pragma unroll
     for (int vt = 0; vt < kVT; ++vt) {
-      // two of W's three parts, from strips of 16 columns: a 16-byte piece per thread and part
+      // W's three parts, from strips of 16 columns: a 16-byte piece per thread and part
       const uint32_t at = s0 + L::kA + vt * 5 * kTileBytes;
       const int r = tid >> 3, p = tid & 7;
       const uint8_t* w = a.w_ws + (hs * (VD / 16) + vt * 4 + (p >> 1)) * (3LL * kStripBytes) + strip_off(p & 1, r);
       cp16(at + 3 * kTileBytes + tile_off(r, p), w, true);
       cp16(at + 4 * kTileBytes + tile_off(r, p), w + kStripBytes, true);
+      cp16(s0 + L::kA3 + 2 * vt * kTileBytes + tile_off(r, p), w + 2 * kStripBytes, true);
     }
     cp_commit();
+  };
+  // one thread's copies of q and k
+  auto load_qk = [&](const GradItem& it) {
+    uint8_t* to = smem + L::kQK;
+    mbar_arrive_expect_tx(qk_full, 2 * kKT * kTileBytes);
+#pragma unroll
+    for (int kt = 0; kt < kKT; ++kt) {
+      tma_load_2d(to + kt * 2 * kTileBytes, &maps.q, it.hk * KD + kt * 64, static_cast<int>(it.t0), qk_full);
+      tma_load_2d(to + (kt * 2 + 1) * kTileBytes, &maps.k, it.hk * KD + kt * 64, static_cast<int>(it.t0), qk_full);
+    }
   };
   auto item_scalars = [&](int buf) { return smem + L::kScal + buf * L::kItem; };
   // four warps, `part` 0..3
@@ -206,49 +229,67 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
   if (tid == 0) {
     mbar_init(bar, 1);
     mbar_init(full, 1);
+    mbar_init(qk_full, 1);
+    mbar_init(kk_done, 1);
     fence_barrier_init();
   }
-  load_tiles(cur, 0);
+  load_tiles(cur);
   if (warp < 4) load_scalars(cur, 0, warp);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tslot;
   const uint32_t mine = tmem + (static_cast<uint32_t>(warp & 3) << 21);  // this warp's lanes
-  const uint32_t aA = s0 + L::kA, big = s0 + L::kBig;
+  const uint32_t aA = s0 + L::kA, a3 = s0 + L::kA3, qk = s0 + L::kQK, big = s0 + L::kBig;
   uint32_t phase = 0, arrived = 0;
   bool alive = true;
+  auto wait_on = [&](uint64_t* b, uint32_t parity, unsigned bit) {
+    if (alive) alive = mbar_spin(b, parity, a.err, bit);
+  };
   auto wait_mma = [&]() {
-    if (alive) alive = mbar_spin(bar, phase, a.err, kErrWaitMma);
+    wait_on(bar, phase, kErrWaitMma);
     phase ^= 1u;
     tc_fence_after();
   };
-  // a state in fragment order -> hi and lo tiles [v][k], four 8 x 8 matrices a step
-  auto state_tiles = [&](const float4* x) {
+  // a state in fragment order -> the tiles [v][k] of its first two parts, or of all three, four
+  // 8 x 8 matrices a step
+  auto state_tiles = [&](auto parts, const float4* x) {
 #pragma unroll
     for (int i = 0; i < kPair; ++i) {
       const int pr = warp + i * (kGradThreads / 32);
       const int n = (pr % (KD / 16)) * 2 + (lane >> 4);  // this lane's row of a matrix
       const int v = (pr / (KD / 16)) * 16 + (lane & 15);
-      const uint32_t dst = big + ((v >> 6) * kKT + (n >> 3)) * kTileBytes + tile_off(v & 63, n & 7);
-      uint32_t hi[4], lo[4];
-      split2(x[2 * i].x, x[2 * i].y, hi[0], lo[0]);
-      split2(x[2 * i].z, x[2 * i].w, hi[1], lo[1]);
-      split2(x[2 * i + 1].x, x[2 * i + 1].y, hi[2], lo[2]);
-      split2(x[2 * i + 1].z, x[2 * i + 1].w, hi[3], lo[3]);
-      stsm4(dst, hi);
-      stsm4(dst + L::kState / 2, lo);
+      const uint32_t at = ((v >> 6) * kKT + (n >> 3)) * kTileBytes + tile_off(v & 63, n & 7);
+      const float2 y[4] = {make_float2(x[2 * i].x, x[2 * i].y), make_float2(x[2 * i].z, x[2 * i].w),
+                           make_float2(x[2 * i + 1].x, x[2 * i + 1].y),
+                           make_float2(x[2 * i + 1].z, x[2 * i + 1].w)};
+      uint32_t p[3][4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (decltype(parts)::value == 3) {
+          uint32_t t[3];
+          split3(y[e].x, y[e].y, t);
+          p[0][e] = t[0];
+          p[1][e] = t[1];
+          p[2][e] = t[2];
+        } else {
+          split2(y[e].x, y[e].y, p[0][e], p[1][e]);
+        }
+      }
+      stsm4(big + at, p[0]);
+      stsm4(big + at + L::kState / 2, p[1]);
+      if constexpr (decltype(parts)::value == 3) stsm4(qk + at, p[2]);
     }
   };
 
   float acc[kCols];  // dQ or dK of this row
-  int buf = 0, qk_buf = 0;
+  int buf = 0;
+  uint32_t item = 0;  // parity of the barriers of q and k and of their product
   while (true) {
     const int h = cur.hk * group + cur.r;
     const long long hs = cur.slot * a.Hv + h;
     const float2* Gs = reinterpret_cast<const float2*>(item_scalars(buf));
     const float* scal = reinterpret_cast<const float*>(item_scalars(buf) + 512);
-    const uint32_t qk = s0 + L::kQK + qk_buf * L::kQKBytes;
     if (cur.r == 0) {
 #pragma unroll
       for (int i = 0; i < kCols; ++i) acc[i] = 0.f;
@@ -262,16 +303,14 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
         sv[2 * i + 1] = S4[pair_off(i) + 32];
       }
     }
-    state_tiles(sv);
+    state_tiles(std::integral_constant<int, 3>{}, sv);
     cp_wait<0>();
-    if (alive) alive = mbar_spin(full, arrived, a.err, kErrWaitFull);
+    wait_on(full, arrived, kErrWaitFull);
     arrived ^= 1u;
     if (cur.live < kChunk) {
 #pragma unroll
       for (int vt = 0; vt < kVT; ++vt)
         clear_rows<kGradThreads>(smem + L::kA + vt * 5 * kTileBytes, 128, 2, kTileBytes, cur.live, tid);
-      if (cur.r == 0)
-        clear_rows<kGradThreads>(smem + L::kQK + qk_buf * L::kQKBytes, 128, 2 * kKT, kTileBytes, cur.live, tid);
     }
     fence_smem_to_async();
     tc_fence_before();
@@ -280,27 +319,28 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
       tc_fence_after();
       constexpr uint32_t idS = mma_desc<false, true, KD>(), idW = mma_desc<false, false, 64>();
       const uint64_t ad = smem_desc(aA, 16, 1024), sd = smem_desc(big, kTileBytes, 1024);
+      const uint64_t a3d = smem_desc(a3, 16, 1024), s3d = smem_desc(qk, kTileBytes, 1024);
 #pragma unroll
       for (int ks = 0; ks < VD / 16; ++ks) {
         const uint32_t at = (ks >> 2) * 5 * kTileBytes + (ks & 3) * 32;
+        const uint32_t at3 = (ks >> 2) * 2 * kTileBytes + (ks & 3) * 32;
         const uint32_t st = (ks >> 2) * kKT * kTileBytes + (ks & 3) * 2048;
-        const uint64_t a0 = desc_at(ad, at), a1 = desc_at(ad, at + kTileBytes);
+        // [do; dX hi], and as rows 64..127 what dX's second and third parts add
+        const uint64_t x0 = desc_at(ad, at), x1 = desc_at(ad, at + kTileBytes), x2 = desc_at(a3d, at3);
         const uint64_t sh = desc_at(sd, st), sl = desc_at(sd, st + L::kState / 2);
         const uint64_t wh = desc_at(ad, at + 3 * kTileBytes), wl = desc_at(ad, at + 4 * kTileBytes);
-        tc_mma(tmem + kD1, a0, sh, idS, ks > 0);
-        tc_mma(tmem + kD1, a0, sl, idS, true);
-        tc_mma(tmem + kD1b, a1, sh, idS, ks > 0);
-        tc_mma(tmem + kD2, a0, wh, idW, ks > 0);
-        tc_mma(tmem + kD2, a0, wl, idW, true);
-        tc_mma(tmem + kD2b, a1, wh, idW, ks > 0);
-      }
-      if (cur.r == 0) {
-        const uint64_t qd = smem_desc(qk, 16, 1024);
-#pragma unroll
-        for (int ks = 0; ks < KD / 16; ++ks) {
-          const uint32_t at = (ks >> 2) * 2 * kTileBytes + (ks & 3) * 32;
-          tc_mma(tmem + kKK, desc_at(qd, at), desc_at(qd, at + kTileBytes), idW, ks > 0);
-        }
+        tc_mma(tmem + kD1, x0, sh, idS, ks > 0);
+        tc_mma(tmem + kD1, x0, sl, idS, true);
+        tc_mma(tmem + kD1, x0, desc_at(s3d, st), idS, true);
+        tc_mma(tmem + kD1b, x1, sh, idS, ks > 0);
+        tc_mma(tmem + kD1b, x1, sl, idS, true);
+        tc_mma(tmem + kD1b, x2, sh, idS, true);
+        tc_mma(tmem + kD2, x0, wh, idW, ks > 0);
+        tc_mma(tmem + kD2, x0, wl, idW, true);
+        tc_mma(tmem + kD2, x0, x2, idW, true);  // rows 0..63 there: W's third part
+        tc_mma(tmem + kD2b, x1, wh, idW, ks > 0);
+        tc_mma(tmem + kD2b, x1, wl, idW, true);
+        tc_mma(tmem + kD2b, x2, wh, idW, true);
       }
       tc_commit(bar);
     }
@@ -328,8 +368,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
       if (lane == 0) red[warp] = v;
     }
     wait_mma();
-    // ---- D takes S's place
-    state_tiles(dd);
+    // ---- q and k take the place of S's third part, D that of the other two
+    if (tid == 0) load_qk(cur);
+    state_tiles(std::integral_constant<int, 2>{}, dd);
     // E (key side) or F, and the second part of E before its range is used again
     float ef[16];
     tc_load16(mine + kD2 + cq * 16, ef);
@@ -339,6 +380,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
 #pragma unroll
       for (int i = 0; i < 16; ++i) ef[i] += t[i];
     }
+    wait_on(qk_full, item, kErrWaitFull);
+    if (cur.live < kChunk)
+      clear_rows<kGradThreads>(smem + L::kQK, 128, 2 * kKT, kTileBytes, cur.live, tid);
     fence_smem_to_async();
     tc_fence_before();
     __syncthreads();
@@ -346,7 +390,16 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
     const bool more = nxt.unit < units;
     if (tid == 0) {
       tc_fence_after();
-      constexpr uint32_t idS = mma_desc<false, true, KD>();
+      constexpr uint32_t idS = mma_desc<false, true, KD>(), idK = mma_desc<false, false, 64>();
+      if (cur.r == 0) {
+        const uint64_t qd = smem_desc(qk, 16, 1024);
+#pragma unroll
+        for (int ks = 0; ks < KD / 16; ++ks) {
+          const uint32_t at = (ks >> 2) * 2 * kTileBytes + (ks & 3) * 32;
+          tc_mma(tmem + kKK, desc_at(qd, at), desc_at(qd, at + kTileBytes), idK, ks > 0);
+        }
+      }
+      tc_commit(kk_done);
       const uint64_t ad = smem_desc(aA, 16, 1024), sd = smem_desc(big, kTileBytes, 1024);
 #pragma unroll
       for (int ks = 0; ks < VD / 16; ++ks) {
@@ -366,25 +419,29 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
     uint32_t hi[8], lo[8];
     float run = 0.f;
     if (cq * 16 <= (warp & 1) * 32 + 31) {
-      float kk[16];
-      tc_load16(mine + kKK + cq * 16, kk);
       const float2 G = Gs[tok];
 #pragma unroll
       for (int i = 0; i < 16; i += 2) {
-        float p[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int j = cq * 16 + i + e;
           float v = 0.f;
           if (key_side ? j < tok : j <= tok)
             v = (key_side ? -ef[i + e] : a.scale * ef[i + e]) * (decay_between(G, Gs[j]) * scal[j]);
-          p[e] = v;
-          // running sums over the columns before, in the place of the terms
-          const float m = j < tok ? v * kk[i + e] : 0.f;
-          ef[i + e] = run;
-          run += m;
+          ef[i + e] = v;
         }
-        split2(p[0], p[1], hi[i / 2], lo[i / 2]);
+        split2(ef[i], ef[i + 1], hi[i / 2], lo[i / 2]);
+      }
+      wait_on(kk_done, item, kErrWaitMma);
+      tc_fence_after();
+      float kk[16];
+      tc_load16(mine + kKK + cq * 16, kk);
+      // running sums over the columns before, in the place of the terms
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float m = cq * 16 + i < tok ? ef[i] * kk[i] : 0.f;
+        ef[i] = run;
+        run += m;
       }
     } else {
 #pragma unroll
@@ -409,8 +466,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
           for (int i = 0; i < 16; ++i) t[i] += u[i];
         }
         const int col = cq * kCols + c * 16;
-        const uint8_t* src = smem + L::kQK + qk_buf * L::kQKBytes +
-                             ((col >> 6) * 2 + (key_side ? 1 : 0)) * kTileBytes;
+        const uint8_t* src = smem + L::kQK + ((col >> 6) * 2 + (key_side ? 1 : 0)) * kTileBytes;
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
           const uint4 x = *reinterpret_cast<const uint4*>(src + tile_off(tok, ((col & 63) >> 3) + p));
@@ -468,11 +524,18 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
     }
     // ---- meanwhile the next item's tiles and S, W D^T, and the sums of dg over i >= t
     if (more) {
-      load_tiles(nxt, nxt.r == 0 ? qk_buf ^ 1 : qk_buf);
-      if (tid == 32) {  // S and D are read through registers: into L2 until then
+      load_tiles(nxt);
+      if (tid == 32) {  // S and D are read through registers, q and k wait for their place: into L2
         const long long ns = nxt.slot * a.Hv + nxt.hk * group + nxt.r;
         bulk_prefetch_l2(a.s_ws + ns * KD * VD * 4, KD * VD * 4);
         bulk_prefetch_l2(a.d_ws + ns * KD * VD * 4, KD * VD * 4);
+        if (nxt.r == 0) {
+#pragma unroll
+          for (int kt = 0; kt < kKT; ++kt) {
+            tma_prefetch_2d(&maps.q, nxt.hk * KD + kt * 64, static_cast<int>(nxt.t0));
+            tma_prefetch_2d(&maps.k, nxt.hk * KD + kt * 64, static_cast<int>(nxt.t0));
+          }
+        }
       }
     }
     if (key_side) {
@@ -574,8 +637,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(const __gri
     }
     __syncthreads();
     if (!more) break;
-    if (nxt.r == 0) qk_buf ^= 1;
     buf ^= 1;
+    item ^= 1u;
     cur = nxt;
   }
   if (warp == 0) tmem_free(tmem, 512);

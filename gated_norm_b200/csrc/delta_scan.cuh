@@ -610,8 +610,8 @@ __device__ __forceinline__ void strip_sums(float r[2][2], float* out, const Scan
 //   dY = scale P^T dO + lambda K D    U = dY - N^T (beta dY)    dX = dV = beta U
 //   dbeta = W . U    b = lambda beta (K D) . W  (for dg)
 //   D' = e^{G_C} D + Q^T (scale gamma dO) - K^T (gamma dX)
-// It writes dv, what dX has below BF16, D of every chunk and each strip's share of the two
-// row sums.
+// It writes dv, what dX has below BF16 (two parts more), D of every chunk and each strip's share of
+// the two row sums.
 template <int KD>
 __global__ void __launch_bounds__(kStripThreads, 1)
     delta_scan_bwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constant__ DeltaMaps maps) {
@@ -748,7 +748,7 @@ __global__ void __launch_bounds__(kStripThreads, 1)
       get_fp32(y, lbuf);
       get_fp32(t, ubuf);
       float rb[2][2], rd[2][2];
-      uint32_t xh[4], xl[4];
+      uint32_t x[3][4];  // dX in three parts
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const float2 be = *reinterpret_cast<const float2*>(scal + me.token(i));
@@ -756,15 +756,23 @@ __global__ void __launch_bounds__(kStripThreads, 1)
         rb[i][1] = be.y * fmaf(y[i][1], w[i][1], y[i][3] * w[i][3]);
         rd[i][0] = fmaf(t[i][0], w[i][0], t[i][2] * w[i][2]);
         rd[i][1] = fmaf(t[i][1], w[i][1], t[i][3] * w[i][3]);
-        split2(be.x * t[i][0], be.y * t[i][1], xh[2 * i], xl[2 * i]);
-        split2(be.x * t[i][2], be.y * t[i][3], xh[2 * i + 1], xl[2 * i + 1]);
+        uint32_t p[3], q[3];
+        split3(be.x * t[i][0], be.y * t[i][1], p);
+        split3(be.x * t[i][2], be.y * t[i][3], q);
+#pragma unroll
+        for (int m = 0; m < 3; ++m) {
+          x[m][2 * i] = p[m];
+          x[m][2 * i + 1] = q[m];
+        }
       }
       const int row = me.row();
       const uint8_t* own = stage + St::kW + strip_off(lane & 1, row);
-      const uint4 vh = turn_strip(xh, me.wstrip(sg + St::kW), own);
-      const uint4 vl = turn_strip(xl, me.wstrip(sg + St::kW), own);
-      *reinterpret_cast<uint4*>(a.x_ws + hs * (a.V / 64 * kTileBytes) + (v0 / 64) * kTileBytes +
-                                tile_off(row, ((v0 & 63) >> 3) + (lane & 1))) = vl;
+      const uint4 vh = turn_strip(x[0], me.wstrip(sg + St::kW), own);
+#pragma unroll
+      for (int m = 1; m < 3; ++m)
+        *reinterpret_cast<uint4*>(a.x_ws + ((hs * 2 + m - 1) * (a.V / 64) + v0 / 64) * kTileBytes +
+                                  tile_off(row, ((v0 & 63) >> 3) + (lane & 1))) =
+            turn_strip(x[m], me.wstrip(sg + St::kW), own);
       if (row < live)
         *reinterpret_cast<uint4*>(a.dv + (t0 + row) * a.lddv + static_cast<long long>(h) * a.V + v0 +
                                   (lane & 1) * 8) = vh;

@@ -394,8 +394,8 @@ GNORM_API size_t gnorm_block_bwd_workspace_bytes(int64_t M, int64_t N);
  * zero_tail.  States are FP32 [B, Hv, K, V].  T < 2^31; B, Hv <= 65535.
  *
  * States, the running sums of g and everything on the way from the BF16 inputs to a state, to
- * dv, dbeta and dinitial_state are held to FP32: matrix operands that are not exact in BF16 are
- * cut into three BF16 parts (24 bits).  Where a product reaches only o, dq, dk or dg, two parts
+ * dv, dg, dbeta and dinitial_state are held to FP32: matrix operands that are not exact in BF16
+ * are cut into three BF16 parts (24 bits).  Where a product reaches only o, dq or dk, two parts
  * (17 bits) are taken.  Results are bitwise the same from run to run.  A value that is not
  * finite reaches its own sequence and value head only (and the tokens before it in its chunk of
  * 64); dq and dk are shared by the value heads of a key head.
@@ -445,8 +445,9 @@ GNORM_API int gnorm_delta_fwd(const gnorm_delta_fwd_desc* desc, void* stream);
  * inputs, writes dq, dk, dv (BF16; dq and dk summed over the value heads of a key head), dg
  * (FP32), dbeta (beta's type) and, unless NULL, dinitial_state.  The forward keeps nothing
  * for it: chunk states are computed again.  workspace:
- * gnorm_delta_workspace_bytes(T, B, Hv, K, V, 1) bytes (about 230 KB per 64 tokens and value
- * head at K = V = 128; the forward's about 32 KB).
+ * gnorm_delta_workspace_bytes(T, B, Hv, K, V, 1) bytes: for each value head T / 64 + B + 1 slots
+ * of 243 KiB at K = V = 128 (the forward's: 31 KiB).  Every sequence, however short, has a slot of
+ * its own: 3000 sequences of one token and 16 heads of 128 x 128 take 11.3 GiB.
  */
 typedef struct gnorm_delta_bwd_desc {
   gnorm_delta_in in;
