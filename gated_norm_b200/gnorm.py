@@ -205,8 +205,8 @@ def workspace(M: int, N: int, deterministic: bool, device, stream=None) -> torch
     """A backward workspace for calls on `stream` of `device` (None = torch's current one), its
     header zero, cached and grown as needed.
 
-    The cache holds one buffer per device and stream, so calls that may run at once do not share
-    one.  A call that is being captured gets a buffer that the graph owns and clears itself: a
+    The cache holds one buffer per device, stream and host thread, so calls that may run at once
+    do not share one, nor do two threads whose calls' kernels mingle on a stream.  A call that is being captured gets a buffer that the graph owns and clears itself: a
     cached one would be in use by eager calls while the graph replays, and its memory another's
     once the cache has grown.
     """
@@ -218,7 +218,7 @@ def workspace(M: int, N: int, deterministic: bool, device, stream=None) -> torch
             buf = torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", idx))
             buf[:256].zero_()
             return buf
-        key = idx, _stream(None, torch.device("cuda", idx))
+        key = idx, _stream(None, torch.device("cuda", idx)), threading.get_ident()
         with _ws_lock:
             buf = _ws_cache.get(key)
             if buf is None or buf.numel() < need:

@@ -122,3 +122,36 @@ def test_two_graphs_at_once_and_a_growing_cache():
             assert float((out[2] - w[2]).abs().max()) <= most
     assert all(bool((t == 3.0).all()) for t in fill)
     assert gn.gnorm_device_error(reset=True) == 0
+
+
+def test_threads_on_one_stream():
+    """The kernels of two threads' calls may mingle on the stream; their workspaces differ."""
+    import threading
+
+    cases = [case(3000, 256, 7), case(5000, 256, 8)]
+    want = [backward(c) for c in cases]
+    torch.cuda.synchronize()
+    got, places, errors = [None, None], [None, None], []
+    start = threading.Barrier(2)
+
+    def work(i):
+        try:
+            x, g, w, dy = cases[i]
+            _, rstd = gn.gnorm_fwd(x, g, w)
+            places[i] = gn.workspace(5000, 256, True, "cuda").data_ptr()
+            start.wait()
+            got[i] = [gn.gnorm_bwd(dy, x, g, w, rstd, dw_fp32=True) for _ in range(200)]
+        except Exception as e:  # shown below
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors and places[0] != places[1]
+    for i in range(2):
+        for out in got[i]:
+            assert_same(out, want[i])
+    assert gn.gnorm_device_error(reset=True) == 0
