@@ -74,7 +74,8 @@ def block_rmsnorm(a, r, w1, w2, eps: float = 1e-6, *, g=None, alpha=None, eps2=N
 
 
 class BlockRMSNorm(torch.nn.Module):
-    """Module form: the two learnable weights and the learnable residual scale (FP32 [1])."""
+    """Module form: the two learnable weights and the learnable residual scale ([1], FP32 in the
+    call whatever type the module has been cast to)."""
 
     def __init__(self, n: int, eps: float = 1e-6, *, alpha: float = 1.0, dtype=torch.bfloat16,
                  device=None):
@@ -86,4 +87,4 @@ class BlockRMSNorm(torch.nn.Module):
 
     def forward(self, a, r, g=None):
         return block_rmsnorm(a, r, self.weight_post, self.weight_pre, self.eps, g=g,
-                             alpha=self.alpha)
+                             alpha=self.alpha.float())
