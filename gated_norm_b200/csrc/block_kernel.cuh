@@ -77,8 +77,13 @@ struct BlockArgs {
 
 // Computing threads and resident CTAs per SM of a row geometry (kind 0 forward, 1 backward).
 // 256 threads; one row group of 512 for the widest rows.  The registers that hold a row's
-// intermediates decide the residency: 3 CTAs of 288 threads leave 72 registers per thread,
-// 2 leave 112, one leaves 224 (at 544 threads: 120).
+// intermediates decide the residency.  The producer's warp, the ninth, takes a further warp's share
+// of one scheduler's registers: 3 CTAs of 288 threads leave 68 registers per thread, 2 leave 96,
+// one leaves 168 (at 544 threads: 96).  The gated backwards spill 28 to 48 bytes a thread with one
+// chunk, 20 to 36 with two and at most 128 threads a row, 0 to 8 with 256 threads a row; with 512
+// threads a row 312 to 336 (two chunks) and 440 to 564 (four), the ungated ones 44 to 84 and 328 to
+// 360: 8192 x 8192 with a gate takes 316 us backward (53% of the measured copy's rate), 4096 x
+// 16384 434 (38%), forward 105 (99%) and 162 (64%).
 GNORM_HD constexpr int block_threads(int tpr) { return tpr > 256 ? tpr : 256; }
 GNORM_HD constexpr int block_ctas_per_sm(int kind, int tpr, int cpt) {
   return tpr > 256 ? 1 : kind == 0 ? (cpt == 1 ? 3 : 2) : (cpt == 1 ? 2 : 1);
@@ -204,7 +209,7 @@ __global__ void __launch_bounds__(block_threads(TPR) + 32, block_ctas_per_sm(0, 
   constexpr int kNCT = block_threads(TPR);
   constexpr int kGroups = kNCT / TPR;
   // Weights stay in registers with one or two chunks per thread; wider rows reload them
-  // (L1-resident) instead of spilling.
+  // (L1-resident; some spill up to 24 bytes a thread all the same).
   constexpr bool kKeepW = CPT <= 2;
   extern __shared__ __align__(128) uint8_t smem[];
   const BlockRing ring = block_ring(smem);
@@ -359,7 +364,7 @@ __global__ void __launch_bounds__(block_threads(TPR) + 32, block_ctas_per_sm(1, 
   // Registers: with 256 threads per CTA the weights and a row's intermediates (hhat, u2,
   // sigmoid) stay in registers between the passes; with 512 the weights are reloaded
   // (L1-resident), and rows of four chunks per thread also recompute the intermediates from
-  // the staged inputs.
+  // the staged inputs (both still spill: block_ctas_per_sm).
   constexpr bool kKeepW = CPT <= 2 && TPR <= 256;
   constexpr bool kKeep = CPT <= 2;
   extern __shared__ __align__(128) uint8_t smem[];

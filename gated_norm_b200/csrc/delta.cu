@@ -133,6 +133,11 @@ cudaError_t launch_cols_fwd(const DeltaArgs& a, const DeltaMaps& m, cudaStream_t
   return launch_grid(delta_cols_fwd_kernel, grid, ColsSmem::kThreads, ColsSmem::kBytes, s, a, m);
 }
 
+// The kernels behind prep read the call's inputs, and cu_seqlens, before they wait for the kernel
+// before.  That is sound because prep, the first of the call, waits for everything older before it
+// lets the next kernel start, and because no kernel of a call writes an input of the call (the
+// entry points refuse outputs that overlap one).  A kernel put before prep, or a prep that does not
+// run, would have to do the same.
 template <int KD>
 cudaError_t run_fwd(const DeltaArgs& a, const DeltaMaps& m, bool whole, int groups, cudaStream_t s) {
   const cudaError_t e = launch_prep<KD>(a, s);

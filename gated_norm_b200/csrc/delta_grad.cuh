@@ -35,8 +35,7 @@
 // another -- S cut and stored, products, D cut and stored, products, pair terms, products -- with
 // one CTA's shared memory and all of tensor memory in use.  S's third part has the place of q and
 // k until its product is done.  Its product first, and q and k copied and multiplied behind the
-// other ones, was slower (forward and backward 1073 us for 1066: the products are issued at the
-// tensor cores' pace and what follows them waits for q.k too).
+// other ones, was slower (forward and backward 1073 us for 1066).
 #pragma once
 
 #include <type_traits>

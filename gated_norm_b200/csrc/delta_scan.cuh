@@ -27,7 +27,7 @@
 //
 // A chunk of 128 x 128 heads takes, with a strip per SM, 2800 cycles without the output and 3400
 // with it (S K 690, X 195, N 740, Y 285, the update 690, the state's parts 150), the backward's
-// 3900: 8192 tokens x 16 heads 198, 232 and 273 us.  One warp issues an m16n8k16 every 14 cycles
+// 3900: 8192 tokens x 16 heads 197, 229 and 279 us.  One warp issues an m16n8k16 every 14 cycles
 // whatever its independent sums, two on a scheduler every 8.  Eight state warps, halves of each
 // product added through shared memory, were slower (253 us for 232), operands fetched a step
 // ahead as well where two strips share an SM (849 us for 780): shared memory, 80% busy there,

@@ -43,7 +43,9 @@ inline cudaError_t ensure_smem_limit(const void* kernel, int bytes) {
 
 // Launch with programmatic stream serialisation: the kernel may be scheduled while the
 // previous kernel on the stream drains; it calls griddepcontrol.wait before touching
-// global memory, so the ordering of memory effects is unchanged.
+// global memory, so the ordering of memory effects is unchanged.  (Kernels behind the first of a
+// call may read the call's inputs before it, where the first one has waited: gnorm_ckpt_step, the
+// delta rule's run_fwd and run_bwd.)
 template <typename Kernel, typename... Args>
 cudaError_t launch_kernel(Kernel kernel, int grid, int block, int smem, cudaStream_t stream,
                           bool pdl, Args... args) {

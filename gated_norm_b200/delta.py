@@ -48,7 +48,8 @@ def gnorm_delta_bwd(do, q, k, v, g, beta, *, scale=None, cu_seqlens=None, initia
 
     dq, dk and dv are BF16, dg is FP32, dbeta has beta's type; dinitial_state is None without
     an initial state.  Rows behind the last sequence are zero in gradients that this call
-    allocates; if any is passed in, they are left as they are in all of them."""
+    allocates and left as they are in ones that are passed in; with cu_seqlens pass all of dq, dk,
+    dv, dg and dbeta, or none."""
     st, *out = _marshal.delta_bwd(do, q, k, v, g, beta, scale, cu_seqlens, initial_state,
                                   dfinal_state, dq, dk, dv, dg, dbeta, dinitial_state,
                                   workspace_buf, _handle(stream))

@@ -32,8 +32,10 @@
  *     programmatic dependent launch, so it may start its prologue while the previous
  *     kernel on the stream drains; it reads and writes global memory only after that
  *     kernel has completed -- except that inside gnorm_ckpt_step the second forward and
- *     the backward may start reading x, g and dy early, which their predecessors in the
- *     same call never write.
+ *     the backward may start reading x, g and dy early, and inside gnorm_delta_fwd and
+ *     gnorm_delta_bwd the kernels behind the first one may start reading q, k, v, d_o,
+ *     cu_seqlens and the incoming states early: the call's own inputs, which their
+ *     predecessors in the same call never write.
  *   - The caller owns every buffer; the library keeps no pointer after a call returns.
  *   - Outputs must not overlap any input or each other (GNORM_ERR_ALIAS).
  *   - Errors are detected on the host before any launch and returned as a gnorm_status;
