@@ -211,20 +211,37 @@ def workspace(M: int, N: int, deterministic: bool, device, stream=None) -> torch
     once the cache has grown.
     """
     device = torch.device(device)
-    idx = device.index if device.index is not None else torch.cuda.current_device()
-    with torch.cuda.device(idx), torch.cuda.stream(stream):  # None: no change
+    if device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    with _on(device):
         need = max(gnorm_bwd_workspace_bytes(M, N, deterministic), 256)
-        if torch.cuda.is_current_stream_capturing():
-            buf = torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", idx))
-            buf[:256].zero_()
-            return buf
-        key = idx, _stream(None, torch.device("cuda", idx)), threading.get_ident()
-        with _ws_lock:
-            buf = _ws_cache.get(key)
-            if buf is None or buf.numel() < need:
-                buf = torch.zeros(need, dtype=torch.uint8, device=torch.device("cuda", idx))
-                _ws_cache[key] = buf
-            return buf
+        if stream is None or stream.cuda_stream == _stream(None, device):
+            return _workspace(need, device)
+        if not isinstance(stream, torch.cuda.Stream):  # another library's
+            stream = torch.cuda.ExternalStream(stream.cuda_stream, device)
+        # what `with torch.cuda.stream(stream)` does, which takes as long as the rest of the call
+        names = "stream_id", "device_index", "device_type"
+        here = dict(zip(names, torch._C._cuda_getCurrentStream(device.index)))
+        torch._C._cuda_setStream(**{n: getattr(stream, n) for n in names})
+        try:
+            return _workspace(need, device)
+        finally:
+            torch._C._cuda_setStream(**here)
+
+
+def _workspace(need: int, device) -> torch.Tensor:
+    """`need` bytes for a call on the current stream of `device`, the current device."""
+    if torch.cuda.is_current_stream_capturing():
+        buf = torch.empty(need, dtype=torch.uint8, device=device)
+        buf[:256].zero_()
+        return buf
+    key = device.index, _stream(None, device), threading.get_ident()
+    with _ws_lock:
+        buf = _ws_cache.get(key)
+        if buf is None or buf.numel() < need:
+            buf = torch.zeros(need, dtype=torch.uint8, device=device)
+            _ws_cache[key] = buf
+        return buf
 
 
 _host_cache: dict = {}

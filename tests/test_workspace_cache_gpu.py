@@ -155,3 +155,19 @@ def test_threads_on_one_stream():
         for out in got[i]:
             assert_same(out, want[i])
     assert gn.gnorm_device_error(reset=True) == 0
+
+
+def test_a_stream_that_is_not_torchs():
+    """Anything with a cuda_stream names the stream, as in the other calls."""
+    from types import SimpleNamespace
+
+    x, g, w, dy = case(300, 128, 9)
+    want = backward((x, g, w, dy))
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    other = SimpleNamespace(cuda_stream=s.cuda_stream)
+    _, rstd = gn.gnorm_fwd(x, g, w, stream=other)
+    got = gn.gnorm_bwd(dy, x, g, w, rstd, dw_fp32=True, stream=other)
+    s.synchronize()
+    assert_same(got, want)
+    assert gn.workspace(300, 128, True, "cuda", other).data_ptr() == gn.workspace(300, 128, True, "cuda", s).data_ptr()
